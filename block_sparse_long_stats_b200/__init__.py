@@ -13,7 +13,10 @@ from .spa import (SpaError, decode, lib, prefill, spa_block_stats, spa_decode_wo
                   spa_select_segperm, spa_prefill_host, spa_prefill_host_workspace_bytes,
                   spa_selftest_wait_timeout, spa_sparse_attn_prefill_segperm,
                   spa_sparse_attn_decode_rla,
-                  spa_select, spa_sparse_attn_decode, spa_sparse_attn_prefill, spa_status_string)
+                  spa_select, spa_sparse_attn_decode, spa_sparse_attn_prefill, spa_status_string,
+                  decode_tree, evict, spa_attn_weight, spa_attn_weight_workspace_bytes,
+                  spa_cache_gather, spa_evict_select, spa_rope, spa_rope_append,
+                  spa_rope_frequencies, spa_sparse_attn_tree, spa_tree_workspace_bytes)
 
 __all__ = ["SpaError", "decode", "lib", "prefill", "spa_block_stats",
            "spa_decode_workspace_bytes", "spa_get_device_error", "spa_last_error",
@@ -24,4 +27,7 @@ __all__ = ["SpaError", "decode", "lib", "prefill", "spa_block_stats",
            "spa_sparse_attn_prefill_segperm",
            "spa_rla_block_states", "spa_rla_decode_state", "spa_rla_decode_workspace_bytes",
            "spa_rla_prefill", "spa_select", "spa_sparse_attn_decode_rla",
-           "spa_sparse_attn_decode", "spa_sparse_attn_prefill", "spa_status_string"]
+           "spa_sparse_attn_decode", "spa_sparse_attn_prefill", "spa_status_string",
+           "decode_tree", "evict", "spa_attn_weight", "spa_attn_weight_workspace_bytes",
+           "spa_cache_gather", "spa_evict_select", "spa_rope", "spa_rope_append",
+           "spa_rope_frequencies", "spa_sparse_attn_tree", "spa_tree_workspace_bytes"]

@@ -1,0 +1,68 @@
+// Launchers of the serving kernels: rotary positions, tree attention, accumulated
+// attention weight, eviction. Arguments are validated in serve_api.cu before any of
+// these is called.
+#pragma once
+
+#include "kernels.h"
+
+namespace spa {
+
+constexpr int kRopeMaxPairs = 128;
+
+struct RopeTensor {
+    const void *x = nullptr;
+    void *y = nullptr;
+    spa_strides xs{0, 0, 0}, ys{0, 0, 0};
+    int H = 0;
+};
+
+// q, k and (append) v of one call; v's rows are copied, not rotated.
+struct RopeCall {
+    RopeTensor t[3];
+    bool bf16 = true;
+    int B = 0, L = 0, d = 0, rot = 0;
+    bool interleaved = false, backward = false, append = false;
+    int T = 0;                          // append: rows of the caches
+    const double *freqs = nullptr;      // host
+    float mscale = 1.f;
+    const int32_t *pos = nullptr, *rows = nullptr;
+    int pos0 = 0;                       // append without rows: the first cache row
+    int *err = nullptr;
+};
+cudaError_t launch_rope(const RopeCall &c, cudaStream_t s);
+
+struct TreeCall {
+    const void *q, *kc, *vc;
+    int B, Hq, Hkv, n, T, d, block, cap;
+    const int32_t *parents, *lens, *idx, *count;
+    float scale;
+    void *workspace, *out;
+    float *lse;
+    int *err;
+};
+size_t tree_workspace_bytes(int B, int Hq, int Hkv, int n, int T, int d, int block);
+cudaError_t launch_tree(const TreeCall &c, cudaStream_t s);
+
+struct WeightCall {
+    const void *q, *k;
+    int B, Hq, Hkv, Lq, T, d, block, cap;
+    const float *lse;
+    const int32_t *lens, *idx, *count;
+    float scale, decay;
+    const float *prev;
+    void *workspace;
+    float *out;
+    int *err;
+};
+size_t weight_workspace_bytes(int B, int Hq, int Lq, int T, int block);
+cudaError_t launch_weight(const WeightCall &c, cudaStream_t s);
+
+cudaError_t launch_evict_select(const float *score, const int32_t *lens, int B, int Hkv, int T,
+                                int n_keep, int n_sink, int n_recent, int32_t *keep,
+                                int32_t *count, int *err, cudaStream_t s);
+cudaError_t launch_cache_gather(const void *kc, const void *vc, const float *score, int B, int Hkv,
+                                int T, int row_bytes, const int32_t *keep, int n_keep,
+                                const int32_t *count, int T_out, void *k_out, void *v_out,
+                                float *score_out, int *err, cudaStream_t s);
+
+}  // namespace spa

@@ -16,7 +16,10 @@ import torch
 __all__ = ["SpaError", "lib", "spa_block_stats", "spa_select", "spa_sparse_attn_prefill",
            "spa_decode_workspace_bytes", "spa_sparse_attn_decode", "spa_get_device_error",
            "spa_status_string", "spa_last_error", "prefill", "decode", "LIB_PATH",
-           "spa_prefill_host", "spa_prefill_host_workspace_bytes", "spa_selftest_wait_timeout"]
+           "spa_prefill_host", "spa_prefill_host_workspace_bytes", "spa_selftest_wait_timeout",
+           "spa_rope_frequencies", "spa_rope", "spa_rope_append", "spa_tree_workspace_bytes",
+           "spa_sparse_attn_tree", "spa_attn_weight_workspace_bytes", "spa_attn_weight",
+           "spa_evict_select", "spa_cache_gather", "decode_tree", "evict"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspa.so")
 
@@ -24,6 +27,8 @@ SPA_F32, SPA_BF16 = 0, 1
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
+_Z = ctypes.c_size_t
 
 _lib = None
 
@@ -85,6 +90,21 @@ def lib() -> ctypes.CDLL:
         L.spa_prefill_host_workspace_bytes.restype = ctypes.c_size_t
         L.spa_prefill_host.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F, _I, _I,
                                        _I, _P, ctypes.c_size_t, _P]
+        L.spa_rope_frequencies.argtypes = [_I, _D, _I, _D, _D, _D, _D, _P, ctypes.POINTER(_F)]
+        L.spa_rope.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
+                               _F, _P, _I, _I, _P]
+        L.spa_rope_append.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                      _I, _I, _I, _P, _F, _P, _P, _I, _P]
+        L.spa_tree_workspace_bytes.argtypes = [_I] * 7
+        L.spa_tree_workspace_bytes.restype = _Z
+        L.spa_sparse_attn_tree.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I,
+                                           _P, _F, _P, _Z, _P, _P, _P]
+        L.spa_attn_weight_workspace_bytes.argtypes = [_I] * 5
+        L.spa_attn_weight_workspace_bytes.restype = _Z
+        L.spa_attn_weight.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _F, _P,
+                                      _F, _P, _Z, _P, _P]
+        L.spa_evict_select.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
+        L.spa_cache_gather.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P]
         L.spa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int)]
         L.spa_selftest_wait_timeout.argtypes = [_I, _P]
         L.spa_status_string.argtypes = [_I]
@@ -97,7 +117,9 @@ def lib() -> ctypes.CDLL:
                   "spa_block_stats_quantized",
                   "spa_sparse_attn_prefill_early_stop", "spa_pbs_permutation", "spa_pbs_gather",
                   "spa_select_segperm", "spa_sparse_attn_prefill_segperm", "spa_prefill_host",
-                  "spa_selftest_wait_timeout"):
+                  "spa_selftest_wait_timeout", "spa_rope_frequencies", "spa_rope",
+                  "spa_rope_append", "spa_sparse_attn_tree", "spa_attn_weight", "spa_evict_select",
+                  "spa_cache_gather"):
             getattr(L, f).restype = _I
         _lib = L
     return _lib
@@ -520,6 +542,295 @@ def spa_sparse_attn_decode(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor, 
     return out
 
 
+# ---------------------------------------------------------------- serving operators
+
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("l", ctypes.c_int64)]
+
+
+class _On:
+    """The device of `t` current, and `stream` (if given) too, so that outputs and
+    workspaces are allocated where they are used; yields the raw stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.dev, self.stream, self.ctx = t.device, stream, None
+        if not t.is_cuda:
+            raise ValueError("libspa works on CUDA tensors only")
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.dev:
+                raise ValueError("the stream is on another device than the tensors")
+            self.ctx = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.dev.index:
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _arg(t: torch.Tensor | None, name: str, shape, dtype, dev) -> int | None:
+    """The address of a dense tensor of exactly this shape, type and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {dev}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _strided(t: torch.Tensor, name: str, shape, dtype, dev):
+    """(address, strides or None where dense) of a [B, H, L, d] view with dense rows."""
+    if t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {dev}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    sb, sh, sl, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"the features of {name} must be contiguous")
+    return t.data_ptr(), ctypes.byref(_Strides(sb, sh, sl))
+
+
+def _layout(layout: str) -> int:
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError(f"unknown rotary layout {layout!r} (half or interleaved)")
+    return _ROPE_LAYOUT[layout]
+
+
+def _rope_freqs(freqs: torch.Tensor) -> int:
+    if freqs.dtype != torch.float64 or freqs.is_cuda or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a one-dimensional float64 tensor on the CPU")
+    return freqs.data_ptr()
+
+
+def spa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none",
+                         factor: float = 1.0, trained: float = 0.0, fast: float = 32.0,
+                         slow: float = 1.0):
+    """Frequencies (float64 [rot/2], CPU) and the factor on the rotated values, for
+    scaling "none", "linear", "ntk" or "parts"."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"unknown scaling {scaling!r} (none, linear, ntk or parts)")
+    freqs = torch.empty(max(rot // 2, 0), dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    _check("spa_rope_frequencies",
+           lib().spa_rope_frequencies(rot, base, _ROPE_SCALING[scaling], factor, trained, fast, slow,
+                                      freqs.data_ptr() or None, ctypes.byref(m)))
+    return freqs, m.value
+
+
+def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscale: float = 1.0,
+             layout: str = "half", pos: torch.Tensor | None = None, pos0: int = 0,
+             backward: bool = False, q_out: torch.Tensor | None = None,
+             k_out: torch.Tensor | None = None, stream=None):
+    """Rotates q [B,Hq,L,d] and k [B,Hkv,L,d] (or None) of any strides with dense rows:
+    -> (q_out, k_out or None), dense unless given. backward: the transposed rotation."""
+    B, Hq, L, d = q.shape
+    dev, dt = q.device, q.dtype
+    with _On(q, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, L, d), device=dev, dtype=dt)
+        qp, qs = _strided(q, "q", q.shape, dt, dev)
+        qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
+        kp = ks = kop = kos = None
+        Hkv = 0
+        if k is not None:
+            Hkv = k.shape[1]
+            shape = (B, Hkv, L, d)
+            if k_out is None:
+                k_out = torch.empty(shape, device=dev, dtype=dt)
+            kp, ks = _strided(k, "k", shape, dt, dev)
+            kop, kos = _strided(k_out, "k_out", shape, dt, dev)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        _check("spa_rope",
+               lib().spa_rope(qp, qs, qop, qos, kp, ks, kop, kos, _dt(q), B, Hq, Hkv, L, d,
+                              2 * freqs.numel(), _layout(layout), _rope_freqs(freqs), mscale,
+                              _arg(pos, "pos", (B, L), torch.int32, dev), pos0, int(backward), st))
+    return q_out, k_out
+
+
+def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch.Tensor,
+                    vc: torch.Tensor, freqs: torch.Tensor, mscale: float = 1.0,
+                    rows: torch.Tensor | None = None, row0: int = 0, layout: str = "half",
+                    pos: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Rotates a step's new q (-> q_out) and k, and writes the rotated k and v into rows
+    rows[b] + t (or row0 + t) of the caches kc, vc [B,Hkv,T,d]."""
+    B, Hq, L, d = q.shape
+    Hkv, T = kc.shape[1], kc.shape[2]
+    dev, dt = q.device, q.dtype
+    with _On(q, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, L, d), device=dev, dtype=dt)
+        qp, qs = _strided(q, "q", q.shape, dt, dev)
+        qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
+        kp, ks = _strided(k, "k", (B, Hkv, L, d), dt, dev)
+        vp, vs = _strided(v, "v", (B, Hkv, L, d), dt, dev)
+        _check("spa_rope_append",
+               lib().spa_rope_append(qp, qs, qop, qos, kp, ks, vp, vs,
+                                     _arg(kc, "kc", (B, Hkv, T, d), dt, dev),
+                                     _arg(vc, "vc", (B, Hkv, T, d), dt, dev), _dt(q), B, Hq, Hkv, L,
+                                     T, d, 2 * freqs.numel(), _layout(layout), _rope_freqs(freqs),
+                                     mscale, _arg(pos, "pos", (B, L), torch.int32, dev),
+                                     _arg(rows, "rows", (B,), torch.int32, dev), row0, st))
+    return q_out
+
+
+def _lists(idx, count, B, Hq, nq, dev):
+    """(address, cap, address) of kept lists, or of none."""
+    if idx is None and count is None:
+        return None, 0, None
+    if idx is None or count is None:
+        raise ValueError("idx and count go together")
+    if idx.dim() != 4:
+        raise ValueError("idx must be [B, Hq, nq, cap]")
+    cap = idx.shape[3]
+    return (_arg(idx, "idx", (B, Hq, nq, cap), torch.int32, dev), cap,
+            _arg(count, "count", (B, Hq, nq), torch.int32, dev))
+
+
+def spa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, T: int, d: int, block: int) -> int:
+    return int(lib().spa_tree_workspace_bytes(B, Hq, Hkv, n, T, d, block))
+
+
+def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
+                         parents: torch.Tensor, block: int, idx: torch.Tensor | None,
+                         count: torch.Tensor | None, scale: float,
+                         lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         want_lse: bool = False, stream=None):
+    """Attention of a tree of n drafted tokens, q [B,Hq,n,d], that sit in the caches
+    [B,Hkv,T,d] behind lens[b] tokens (T - n without lens); parents [B,n] int32, lists as
+    for decode or None. Returns (out, lse or None)."""
+    B, Hq, n, d = q.shape
+    Hkv, T = kc.shape[1], kc.shape[2]
+    dev, dt = q.device, q.dtype
+    with _On(q, stream) as st:
+        need = spa_tree_workspace_bytes(B, Hq, Hkv, n, T, d, block)
+        if workspace is None:
+            workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("the workspace must be contiguous and on the tensors' device")
+        if out is None:
+            out = torch.empty((B, Hq, n, d), device=dev, dtype=dt)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, n), device=dev, dtype=torch.float32)
+        ip, cap, cp = _lists(idx, count, B, Hq, 1, dev)
+        _check("spa_sparse_attn_tree",
+               lib().spa_sparse_attn_tree(_arg(q, "q", q.shape, dt, dev),
+                                          _arg(kc, "kc", (B, Hkv, T, d), dt, dev),
+                                          _arg(vc, "vc", (B, Hkv, T, d), dt, dev), _dt(q), B, Hq, Hkv,
+                                          n, T, d, block, _arg(parents, "parents", (B, n), torch.int32, dev),
+                                          _arg(lens, "lens", (B,), torch.int32, dev), ip, cap, cp,
+                                          scale, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(),
+                                          _arg(out, "out", q.shape, dt, dev),
+                                          _arg(lse, "lse", (B, Hq, n), torch.float32, dev), st))
+    return out, lse
+
+
+def spa_attn_weight_workspace_bytes(B: int, Hq: int, Lq: int, T: int, block: int) -> int:
+    return int(lib().spa_attn_weight_workspace_bytes(B, Hq, Lq, T, block))
+
+
+def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: float,
+                    block: int = 128, idx: torch.Tensor | None = None,
+                    count: torch.Tensor | None = None, lens: torch.Tensor | None = None,
+                    prev: torch.Tensor | None = None, decay: float = 1.0,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Attention weight that the sequence's last Lq queries, q [B,Hq,Lq,d] with their lse
+    [B,Hq,Lq], give every key of k [B,Hkv,T,d], added to decay * prev: [B,Hkv,T] fp32."""
+    B, Hq, Lq, d = q.shape
+    Hkv, T = k.shape[1], k.shape[2]
+    dev, dt = q.device, q.dtype
+    with _On(q, stream) as st:
+        ip, cap, cp = None, 0, None
+        if idx is not None or count is not None:
+            nq = (T - 1) // block - (T - Lq) // block + 1 if block > 0 else 0
+            ip, cap, cp = _lists(idx, count, B, Hq, nq, dev)
+            if workspace is None:
+                need = spa_attn_weight_workspace_bytes(B, Hq, Lq, T, block)
+                workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
+        wp, wn = None, 0
+        if workspace is not None:
+            if not workspace.is_contiguous() or workspace.device != dev:
+                raise ValueError("the workspace must be contiguous and on the tensors' device")
+            wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if out is None:
+            out = torch.empty((B, Hkv, T), device=dev, dtype=torch.float32)
+        _check("spa_attn_weight",
+               lib().spa_attn_weight(_arg(q, "q", q.shape, dt, dev), _arg(k, "k", (B, Hkv, T, d), dt, dev),
+                                     _dt(q), B, Hq, Hkv, Lq, T, d,
+                                     _arg(lse, "lse", (B, Hq, Lq), torch.float32, dev),
+                                     _arg(lens, "lens", (B,), torch.int32, dev), block, ip, cap, cp, scale,
+                                     _arg(prev, "prev", (B, Hkv, T), torch.float32, dev), decay, wp, wn,
+                                     _arg(out, "out", (B, Hkv, T), torch.float32, dev), st))
+    return out
+
+
+def spa_evict_select(score: torch.Tensor, n_keep: int, n_sink: int = 4, n_recent: int = 0,
+                     lens: torch.Tensor | None = None, keep: torch.Tensor | None = None,
+                     count: torch.Tensor | None = None, stream=None):
+    """The n_keep keys of score [B,Hkv,T] fp32 that stay: ascending keep [B,Hkv,n_keep] int32
+    (-1 behind the last) and count [B] int32."""
+    B, Hkv, T = score.shape
+    dev = score.device
+    with _On(score, stream) as st:
+        if keep is None:
+            keep = torch.empty((B, Hkv, max(n_keep, 0)), device=dev, dtype=torch.int32)
+        if count is None:
+            count = torch.empty((B,), device=dev, dtype=torch.int32)
+        _check("spa_evict_select",
+               lib().spa_evict_select(_arg(score, "score", (B, Hkv, T), torch.float32, dev),
+                                      _arg(lens, "lens", (B,), torch.int32, dev), B, Hkv, T, n_keep, n_sink,
+                                      n_recent, _arg(keep, "keep", (B, Hkv, n_keep), torch.int32, dev),
+                                      _arg(count, "count", (B,), torch.int32, dev), st))
+    return keep, count
+
+
+def spa_cache_gather(kc: torch.Tensor, vc: torch.Tensor, keep: torch.Tensor,
+                     count: torch.Tensor | None = None, score: torch.Tensor | None = None,
+                     k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                     score_out: torch.Tensor | None = None, stream=None):
+    """The rows of kc, vc [B,Hkv,T,d] (and of score) that keep [B,Hkv,n_keep] names, closed up
+    in k_out, v_out [B,Hkv,T_out,d] (T_out >= n_keep; new ones of n_keep rows, zero behind
+    the last, where none are given). Returns (k_out, v_out, score_out or None)."""
+    B, Hkv, T, d = kc.shape
+    n_keep = keep.shape[2]
+    dev, dt = kc.device, kc.dtype
+    with _On(kc, stream) as st:
+        new = torch.zeros if count is not None else torch.empty
+        if k_out is None:
+            k_out = new((B, Hkv, n_keep, d), device=dev, dtype=dt)
+        T_out = k_out.shape[2]
+        if v_out is None:
+            v_out = new((B, Hkv, T_out, d), device=dev, dtype=dt)
+        if score_out is None and score is not None:
+            score_out = new((B, Hkv, T_out), device=dev, dtype=torch.float32)
+        _check("spa_cache_gather",
+               lib().spa_cache_gather(_arg(kc, "kc", (B, Hkv, T, d), dt, dev),
+                                      _arg(vc, "vc", (B, Hkv, T, d), dt, dev),
+                                      _arg(score, "score", (B, Hkv, T), torch.float32, dev), _dt(kc), B, Hkv,
+                                      T, d, _arg(keep, "keep", (B, Hkv, n_keep), torch.int32, dev), n_keep,
+                                      _arg(count, "count", (B,), torch.int32, dev), T_out,
+                                      _arg(k_out, "k_out", (B, Hkv, T_out, d), dt, dev),
+                                      _arg(v_out, "v_out", (B, Hkv, T_out, d), dt, dev),
+                                      _arg(score_out, "score_out", (B, Hkv, T_out), torch.float32, dev), st))
+    return k_out, v_out, score_out
+
+
 def spa_selftest_wait_timeout(limit_us: int, stream=None) -> None:
     """Enqueues the bounded-wait self-test: a wait that nothing completes runs out
     after limit_us and records SPA_DEVERR_TIMEOUT (read it with spa_get_device_error)."""
@@ -536,19 +847,27 @@ def spa_get_device_error() -> int:
 
 
 def prefill(q, k, v, block: int, top_p: float, scale: float | None = None, n_sink: int = 1,
-            n_local: int = 1, k_min: int = 0, want_lse: bool = False, stream=None):
-    """The whole prefill path: block stats -> selection -> sparse attention.
+            n_local: int = 1, k_min: int = 0, want_lse: bool = False, stream=None, rope=None,
+            rope_layout: str = "half"):
+    """The whole prefill path: (rotary positions) -> block stats -> selection -> sparse
+    attention.
 
-    Returns dict(out, lse, idx, count, mean, var).
+    rope: None, or the (freqs, mscale) of spa_rope_frequencies for q and k that are not
+    rotated yet (of any strides with dense rows).
+    Returns dict(out, lse, idx, count, mean, var), with rope also the rotated q and k.
     """
     T = k.shape[2]
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    rotated = {}
+    if rope is not None:
+        q, k = spa_rope(q, k, *rope, layout=rope_layout, stream=stream)
+        rotated = {"q": q, "k": k}
     mean, var = spa_block_stats(k, block, stream=stream)
     idx, count = spa_select(q, mean, var, T, block, scale, top_p, n_sink, n_local, k_min,
                             stream=stream)
     out, lse = spa_sparse_attn_prefill(q, k, v, block, idx, count, scale, want_lse=want_lse,
                                        stream=stream)
-    return {"out": out, "lse": lse, "idx": idx, "count": count, "mean": mean, "var": var}
+    return {"out": out, "lse": lse, "idx": idx, "count": count, "mean": mean, "var": var, **rotated}
 
 
 def decode(q, kc, vc, block: int, top_p: float, mean=None, var=None, scale: float | None = None,
@@ -563,3 +882,34 @@ def decode(q, kc, vc, block: int, top_p: float, mean=None, var=None, scale: floa
     out = spa_sparse_attn_decode(q, kc, vc, block, idx, count, scale, workspace=workspace,
                                  stream=stream)
     return {"out": out, "idx": idx, "count": count, "mean": mean, "var": var}
+
+
+def decode_tree(q, kc, vc, parents, block: int, top_p: float, mean=None, var=None,
+                scale: float | None = None, n_sink: int = 1, n_local: int = 1, k_min: int = 0,
+                workspace=None, want_lse: bool = False, stream=None):
+    """One step over a tree of n drafted tokens, in the last n rows of the caches: (stats, if
+    not given) -> selection by node 0's query -> tree attention over the kept blocks.
+
+    Returns dict(out, lse, idx, count, mean, var).
+    """
+    T = kc.shape[2]
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    with _On(q, stream):
+        root = q[:, :, :1].contiguous()
+        if mean is None or var is None:
+            mean, var = spa_block_stats(kc, block)
+        idx, count = spa_select(root, mean, var, T, block, scale, top_p, n_sink, n_local, k_min)
+        out, lse = spa_sparse_attn_tree(q, kc, vc, parents, block, idx, count, scale,
+                                        workspace=workspace, want_lse=want_lse)
+    return {"out": out, "lse": lse, "idx": idx, "count": count, "mean": mean, "var": var}
+
+
+def evict(kc, vc, score, n_keep: int, n_sink: int = 4, n_recent: int = 0, lens=None, stream=None):
+    """A smaller cache of the n_keep keys per kv-head with the most accumulated attention
+    weight: choice -> move.
+
+    Returns dict(k, v, score, keep, count).
+    """
+    keep, count = spa_evict_select(score, n_keep, n_sink, n_recent, lens=lens, stream=stream)
+    k, v, score = spa_cache_gather(kc, vc, keep, count, score=score, stream=stream)
+    return {"k": k, "v": v, "score": score, "keep": keep, "count": count}

@@ -10,6 +10,14 @@
  *   spa_rla_block_states / spa_rla_prefill, spa_rla_decode_state /
  *   spa_sparse_attn_decode_rla -> (optional) linear attention with an
  *                       exponential feature map over the blocks left out
+ * Around it, for serving:
+ *   spa_rope / spa_rope_append -> rotary positions of q and k before the above, and
+ *                       the append of new tokens to a cache
+ *   spa_sparse_attn_tree -> attention of a tree of drafted tokens over the kept
+ *                       blocks of a cache
+ *   spa_attn_weight, spa_evict_select, spa_cache_gather -> the attention weight that
+ *                       every cached key accumulates, and a smaller cache of the keys
+ *                       with the most of it
  *
  * Conventions shared by every call
  *   - All tensors are dense, contiguous, row-major, in DEVICE memory (spa_prefill_host:
@@ -63,8 +71,9 @@ typedef enum { SPA_QFMT_INT4 = 0, SPA_QFMT_FP4 = 1 } spa_qformat;
 
 /* Device-side error codes reported by spa_get_device_error. */
 #define SPA_DEVERR_NONE 0
-#define SPA_DEVERR_BAD_INDEX 1   /* kept-list entry out of range or not ascending: skipped */
-#define SPA_DEVERR_BAD_COUNT 2   /* count < 0 or > cap: clamped */
+#define SPA_DEVERR_BAD_INDEX 1   /* kept-list entry out of range or not ascending, cache row or
+                                    tree parent out of range: skipped */
+#define SPA_DEVERR_BAD_COUNT 2   /* count < 0 or > cap, or a length outside its range: clamped */
 #define SPA_DEVERR_TIMEOUT 3     /* a bounded wait on an mbarrier ran out: the kernel quit */
 
 typedef void *spa_stream; /* cudaStream_t */
@@ -461,6 +470,192 @@ spa_status spa_prefill_host(const void *q, const void *k, const void *v, void *o
                             int B, int Hq, int Hkv, int L, int d, int block, float scale,
                             float top_p, int n_sink, int n_local, int k_min, void *workspace,
                             size_t workspace_bytes, spa_stream stream);
+
+/*
+ * Rotary positions. Pair c of a head's first `rot` features, (x1, x2), turns by the
+ * angle pos * freqs[c] and is scaled by mscale:
+ *   y1 = mscale (x1 cos - x2 sin),   y2 = mscale (x2 cos + x1 sin)
+ * SPA_ROPE_HALF pairs feature c with c + rot/2, SPA_ROPE_INTERLEAVED 2c with 2c + 1.
+ * Features rot .. d-1 are copied.
+ *
+ * spa_rope_frequencies fills freqs[rot/2] (radians per position, host memory) and
+ * *mscale for
+ *   SPA_ROPE_NONE    freqs[c] = base^(-2c/rot), mscale = 1
+ *   SPA_ROPE_LINEAR  those over `factor` (positions interpolated)
+ *   SPA_ROPE_NTK     base replaced by base * factor^(rot/(rot-2)): the slowest pair is
+ *                    interpolated, the fastest kept
+ *   SPA_ROPE_PARTS   pairs that turn at least `fast` times over the trained length are
+ *                    kept, those that turn at most `slow` times interpolated, a linear
+ *                    ramp over c between; mscale = 1 + 0.1 ln(factor)
+ *   rot: even, 2 .. 256 (NTK: at least 4); base > 1; factor >= 1; PARTS: trained > 0,
+ *   fast > slow > 0 (ignored otherwise). SPA_ERR_INVALID if not. Touches no device.
+ */
+typedef enum { SPA_ROPE_HALF = 0, SPA_ROPE_INTERLEAVED = 1 } spa_rope_layout;
+typedef enum {
+    SPA_ROPE_NONE = 0,
+    SPA_ROPE_LINEAR = 1,
+    SPA_ROPE_NTK = 2,
+    SPA_ROPE_PARTS = 3
+} spa_rope_scaling;
+spa_status spa_rope_frequencies(int rot, double base, spa_rope_scaling scaling, double factor,
+                                double trained, double fast, double slow, double *freqs,
+                                float *mscale);
+
+/*
+ * Element strides of a [B, H, L, d] view: of the batch, the head and the row. The d
+ * features of a row are contiguous.
+ */
+typedef struct {
+    int64_t b, h, l;
+} spa_strides;
+
+/*
+ * spa_rope: rotates q and, in the same launch, k (k = k_out = NULL: q alone).
+ *   q [B, Hq, L, d], k [B, Hkv, L, d], dt, with strides q_str, k_str (NULL: dense);
+ *   so a fused projection's [B, L, heads, d] output is read in place
+ *   q_out, k_out : the same shapes, with strides qo_str, ko_str (NULL: dense). An
+ *            output may be its own input with the same strides; it must not overlap
+ *            an input otherwise
+ *   rot    : even, 2 <= rot <= d;  d <= 256
+ *   freqs  : HOST array of rot/2 doubles, read before the call returns
+ *   pos    : device int32 [B, L], any values, or NULL: row t is at pos0 + t
+ *   backward : 0, or 1 for the transposed rotation: with the output's gradient as q
+ *            (and k), the input's gradient
+ * Angles are reduced in fp64, so far positions keep their accuracy; the rotation is
+ * fp32, rounded once. No alignment is asked for: 16-byte accesses are used where
+ * bases and strides allow them.
+ */
+spa_status spa_rope(const void *q, const spa_strides *q_str, void *q_out,
+                    const spa_strides *qo_str, const void *k, const spa_strides *k_str,
+                    void *k_out, const spa_strides *ko_str, spa_dtype dt, int B, int Hq, int Hkv,
+                    int L, int d, int rot, spa_rope_layout layout, const double *freqs,
+                    float mscale, const int32_t *pos, int pos0, int backward, spa_stream stream);
+
+/*
+ * spa_rope_append: the same rotation of a step's new tokens, with their keys and
+ * values appended to a cache in the same launch: q_out = rotated q,
+ *   kc[b, g, row + t, :] = rotated k[b, g, t, :],  vc[b, g, row + t, :] = v[b, g, t, :]
+ * with row = rows[b] (device int32 [B]) or, where rows is NULL, row0.
+ *   v [B, Hkv, L, d] with strides v_str; kc, vc: [B, Hkv, T, d] dense, overlapping no
+ *   input; every other row of the caches is left as it was. pos NULL: token t of
+ *   sequence b is at position row + t. A row outside [0, T) is not written and
+ *   recorded as SPA_DEVERR_BAD_INDEX. Other arguments as spa_rope.
+ */
+spa_status spa_rope_append(const void *q, const spa_strides *q_str, void *q_out,
+                           const spa_strides *qo_str, const void *k, const spa_strides *k_str,
+                           const void *v, const spa_strides *v_str, void *kc, void *vc,
+                           spa_dtype dt, int B, int Hq, int Hkv, int L, int T, int d, int rot,
+                           spa_rope_layout layout, const double *freqs, float mscale,
+                           const int32_t *pos, const int32_t *rows, int row0, spa_stream stream);
+
+/*
+ * Attention of a tree of n drafted tokens per sequence over the kept blocks of a KV
+ * cache that already holds them. Node i of sequence b sits in cache row len + i, with
+ * len = lens[b] tokens before the tree. It attends to
+ *   - the keys u < len whose block is on its head's list (every key without lists), and
+ *   - itself and its ancestors in the tree, whether their blocks are kept or not:
+ *   out[b,h,i,:] = sum_u softmax_u(s q_i.k_u) v_u,   lse[b,h,i] = log sum_u exp(s q_i.k_u)
+ * A single token is the tree of one node (n = 1, parent -1), drafts in a line have
+ * parents i - 1.
+ *   q       : [B, Hq, n, d];  kc, vc : [B, Hkv, T, d];  dt = SPA_BF16, d = 64 or 128,
+ *             1 <= n <= 128, n <= T, at most 16 query heads per kv-head
+ *   parents : device int32 [B, n]: the parent's node number (smaller than the node's
+ *             own), -1 for a child of the committed text, less than -1 for an unused
+ *             node (smaller trees of a batch), which attends to nothing: out = 0 and
+ *             lse = -inf. A parent that is not smaller than its node is recorded as
+ *             SPA_DEVERR_BAD_INDEX and its node treated as unused; so are the
+ *             descendants of an unused node, without a record.
+ *   lens    : device int32 [B], 0 <= lens[b] <= T - n, or NULL: T - n for all. Outside:
+ *             clamped, recorded as SPA_DEVERR_BAD_COUNT. Rows from lens[b] + n on, and
+ *             the rows of unused nodes, may hold anything, NaN included.
+ *   idx, count : [B, Hq, 1, cap], [B, Hq, 1] ascending lists of blocks of `block` keys (16,
+ *             32, 64 or 128), as spa_select gives them with Lq = 1 (cap >= ceil(T/block)),
+ *             one list for all nodes; both NULL: every block. Blocks at or after len
+ *             are allowed and add nothing.
+ *   workspace : >= spa_tree_workspace_bytes(...) device bytes, 16-byte aligned,
+ *             overwritten; calls that may overlap in time need one each
+ *   out     : [B, Hq, n, d] bf16;  lse : [B, Hq, n] fp32 or NULL (natural log)
+ * P is rounded to bf16 for the PV product, as in spa_sparse_attn_prefill; sums and
+ * the softmax state are fp32. A non-finite value in a kept block or a used node's row
+ * may reach every query of its kv-head.
+ */
+size_t spa_tree_workspace_bytes(int B, int Hq, int Hkv, int n, int T, int d, int block);
+spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, spa_dtype dt, int B,
+                                int Hq, int Hkv, int n, int T, int d, int block,
+                                const int32_t *parents, const int32_t *lens, const int32_t *idx,
+                                int cap, const int32_t *count, float scale, void *workspace,
+                                size_t workspace_bytes, void *out, float *lse, spa_stream stream);
+
+/*
+ * Attention weight that every key receives, summed over queries and the query heads
+ * of its kv-head and added to what it had before:
+ *   out[b,g,t] = decay prev[b,g,t]
+ *                + sum_{h of g, i} exp(s q_{b,h,i}.k_{b,g,t} - lse[b,h,i])
+ * over the queries that see t: the Lq queries are the last of the sequence, query i at
+ * position len - Lq + i, and see t <= that position (t in a block their list keeps,
+ * where lists are given).
+ *   q   : [B, Hq, Lq, d];  k : [B, Hkv, T, d];  dt = SPA_BF16, d = 64 or 128,
+ *         1 <= Lq <= T, at most 16 query heads per kv-head
+ *   lse : [B, Hq, Lq] fp32, natural: what spa_sparse_attn_prefill or
+ *         spa_sparse_attn_tree wrote for the same queries, keys and lists. A row of
+ *         -inf (it saw nothing) adds nothing.
+ *   lens : device int32 [B], Lq <= lens[b] <= T, or NULL: T. Outside: clamped, recorded
+ *         as SPA_DEVERR_BAD_COUNT. Keys from lens[b] on get no weight (out = decay
+ *         prev), whatever their rows hold.
+ *   idx, count : NULL, or the lists of the query blocks that the Lq rows touch,
+ *         [B, Hq, nq, cap], [B, Hq, nq] with nq = (T-1)/block - (T-Lq)/block + 1: those of
+ *         prefill for Lq = T, of decode for Lq = 1. With lists, lens has to be NULL or
+ *         Lq = 1. cap >= ceil(T/block). block: 16, 32, 64 or 128 (read with lists only)
+ *   prev : [B, Hkv, T] fp32 or NULL (zero);  decay : finite
+ *   out  : [B, Hkv, T] fp32, may be prev
+ *   workspace : >= spa_attn_weight_workspace_bytes(...) (0 without lists: may be NULL),
+ *         16-byte aligned, overwritten; calls that may overlap in time need one each
+ * Products are accumulated in fp32, weights and their sums fp32; no atomics, so calls
+ * repeat bit for bit.
+ */
+size_t spa_attn_weight_workspace_bytes(int B, int Hq, int Lq, int T, int block);
+spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, int B, int Hq, int Hkv,
+                           int Lq, int T, int d, const float *lse, const int32_t *lens, int block,
+                           const int32_t *idx, int cap, const int32_t *count, float scale,
+                           const float *prev, float decay, void *workspace,
+                           size_t workspace_bytes, float *out, spa_stream stream);
+
+/*
+ * Eviction, the choice: the n_keep keys of each (b, kv-head) that stay. The first
+ * n_sink and the last n_recent of the len = lens[b] keys always do, then those with
+ * the largest score (equal scores, -0 and +0 among them: the smaller index; NaN counts
+ * as less than every number). If len <= n_keep all keys stay.
+ *   score : [B, Hkv, T] fp32 (spa_attn_weight's output)
+ *   lens  : device int32 [B], 0 <= lens[b] <= T, or NULL: T. Outside: clamped, recorded
+ *           as SPA_DEVERR_BAD_COUNT
+ *   1 <= n_keep, n_sink + n_recent <= n_keep
+ *   keep  : [B, Hkv, n_keep] int32, ascending; entries from count[b] on are -1
+ *   count : [B] int32 = min(lens[b], n_keep): the lengths of the smaller cache
+ */
+spa_status spa_evict_select(const float *score, const int32_t *lens, int B, int Hkv, int T,
+                            int n_keep, int n_sink, int n_recent, int32_t *keep, int32_t *count,
+                            spa_stream stream);
+
+/*
+ * Eviction, the move: the kept rows of K, V and their scores, closed up in a smaller
+ * cache (also for the drafted tokens that were accepted, with a list of them):
+ *   k_out[b,g,i,:] = kc[b,g,keep[b,g,i],:] for i < count[b], v_out, score_out likewise
+ *   kc, vc : [B, Hkv, T, d] of dt (d * element size a multiple of 16 bytes);
+ *   score  : [B, Hkv, T] fp32 or NULL (with score_out)
+ *   keep   : [B, Hkv, n_keep] int32, entries in [0, T) in any order;  count : [B], or NULL:
+ *            n_keep. An entry out of range is not copied and recorded as
+ *            SPA_DEVERR_BAD_INDEX, a count outside [0, n_keep] clamped and recorded as
+ *            SPA_DEVERR_BAD_COUNT.
+ *   k_out, v_out : [B, Hkv, T_out, d], T_out >= n_keep; score_out : [B, Hkv, T_out]. They
+ *            must not overlap the inputs (an exact same pointer is SPA_ERR_INVALID). Rows
+ *            from count[b] on are left as they were.
+ * Keys keep the rotary positions they were written with; block statistics of the
+ * smaller cache are those of spa_block_stats on it.
+ */
+spa_status spa_cache_gather(const void *kc, const void *vc, const float *score, spa_dtype dt, int B,
+                            int Hkv, int T, int d, const int32_t *keep, int n_keep,
+                            const int32_t *count, int T_out, void *k_out, void *v_out,
+                            float *score_out, spa_stream stream);
 
 /*
  * Reads and clears the device error word of the current device (one of
