@@ -1,5 +1,29 @@
-// Attention of a tree of drafted tokens over the kept blocks of a KV cache (bf16).
-// One CTA per (b, query head, node), 128 keys at a time with the online softmax.
+// Attention of a tree of drafted tokens over the kept blocks of a KV cache (bf16), on
+// the sm_100a tensor cores.
+//
+//   out_i = sum_u softmax_u(s q_i.k_u) v_u over the kept cached keys and the ancestors
+//
+// The rows of a problem are the G n queries of a (b, kv-head): they lie next to each
+// other in q, and all of them read the same keys, so K and V cross HBM once for up to
+// 256 rows. Decode with a few drafted tokens is bound by those bytes (512 per key
+// against 4 G n d flops); from about 200 rows on the tensor cores and the exponentials
+// take as long.
+//
+// Work is counted in tiles of 128 keys (kept blocks of the list, closed up; the tree
+// itself is the last tile of its sequence) and the tiles of all (b, kv-head, row tile)
+// units in a row are cut into equal runs, one per CTA and SM, whatever the sequences'
+// lengths: a run may end inside a unit and go on in the next one. A unit that lies in
+// several runs leaves one (m, l, O) state per run in the workspace, and a second kernel
+// joins them.
+//
+// A CTA has two softmax warpgroups with a score tile S and an output tile O in tensor
+// memory each. With up to 128 rows the warpgroups take the key tiles in turn, each with
+// an own state for all rows, joined at the end (RT = 1); with more rows they work on
+// the same key tile, each for its own 128 rows (RT = 2). Either way one warpgroup's
+// exponentials run beside the other's products. Warp roles:
+//   warps 0-3, 4-7 : softmax; thread r of a warpgroup owns row r = TMEM lane r
+//   warp 8         : TMA producer (Q per unit; rings of K and of V tiles)
+//   warp 9         : TMEM allocator and tcgen05.mma issuer
 #include <math.h>
 
 #include "serve.h"
@@ -7,101 +31,753 @@
 namespace spa {
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) tree_kernel(TreeCall a) {
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
-    const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(a.kc);
-    const __nv_bfloat16 *vc = static_cast<const __nv_bfloat16 *>(a.vc);
-    __shared__ float qs[D], ps[128], red[4];
-    __shared__ int key_s[128];
-    const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const int g = h / (a.Hq / a.Hkv);
-    const size_t row = ((size_t)b * a.Hq + h) * a.n + i;
-    const int32_t *par = a.parents + (size_t)b * a.n;
-    if (tid < D) qs[tid] = __bfloat162float(q[row * D + tid]);
-    int P = a.lens ? a.lens[b] : a.T - a.n;
-    if (P < 0 || P > a.T - a.n) {
-        set_error(a.err, SPA_DEVERR_BAD_COUNT);
-        P = P < 0 ? 0 : a.T - a.n;
+constexpr int kCtas = 148;             // one per SM
+constexpr int kThreads = 320;
+constexpr int kTile = 128;             // keys
+constexpr int kMinTiles = 2;           // tiles a run has at least
+constexpr int kRange = 4096;           // blocks whose list is held in shared memory
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+
+struct TreeArgs {
+    const int32_t *parents, *lens, *idx, *count;
+    __nv_bfloat16 *out;
+    float *lse, *ws_o, *ws_ml;
+    int B, Hq, Hkv, G, n, T, cap, nrt;   // nrt: row tiles per (b, kv-head)
+    float scale_log2;
+    int *err;
+};
+
+template <int D, int BLK, int RT>
+struct Cfg {
+    static constexpr int PER = kTile / BLK;            // blocks per tile
+    static constexpr int HALVES = D / 64;              // 64-column halves (128-byte swizzle)
+    static constexpr int HALF = kTile * 128;           // bytes of one
+    static constexpr int SLOT = HALVES * HALF;         // a K or V tile, a Q row tile
+    static constexpr int NK = D == 64 ? 4 : (RT == 1 ? 3 : 2);
+    static constexpr int NV = D == 64 ? 4 : 2;
+    static constexpr int OFF_K = RT * SLOT;
+    static constexpr int OFF_V = OFF_K + NK * SLOT;
+    static constexpr int OFF_LIST = OFF_V + NV * SLOT; // uint32 [kRange]: head mask, block
+    static constexpr int OFF_MARK = OFF_LIST + kRange * 4;   // uint16 [kRange]
+    static constexpr int SMEM = OFF_MARK + kRange * 2 + 1024;
+    static constexpr uint32_t IDESC_S = idesc_bf16(128, kTile, false);
+    static constexpr uint32_t IDESC_O = idesc_bf16(128, D, true);
+};
+
+// Text length before the tree, clamped to the cache.
+__device__ __forceinline__ int text_len(const TreeArgs &a, int b) {
+    const int p = a.lens ? __ldg(a.lens + b) : a.T - a.n;
+    return min(max(p, 0), a.T - a.n);
+}
+__device__ __forceinline__ int tiles_of(const TreeArgs &a, int b) {
+    return (text_len(a, b) + kTile - 1) / kTile + 1;
+}
+
+// The runs: tiles in all (below 2^31: the rows of the caches are), tiles per CTA, and
+// where a tile lies. Every lane of a warp calls these together.
+struct Where {
+    int b, unit, t;      // sequence, unit (b-major, then kv-head, then row tile), tile of the unit
+};
+__device__ __forceinline__ int run_total(const TreeArgs &a) {
+    const int lane = threadIdx.x & 31, upb = a.Hkv * a.nrt;
+    if (!a.lens) return a.B * upb * tiles_of(a, 0);
+    int s = 0;
+    for (int b = lane; b < a.B; b += 32) s += tiles_of(a, b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s * upb;
+}
+__device__ __forceinline__ int run_chunk(int total) { return max(kMinTiles, (total + kCtas - 1) / kCtas); }
+__device__ __forceinline__ Where locate(const TreeArgs &a, int pos) {
+    const int lane = threadIdx.x & 31, upb = a.Hkv * a.nrt;
+    Where w;
+    if (!a.lens) {
+        const int tb = tiles_of(a, 0);
+        w.unit = pos / tb;
+        w.t = pos - w.unit * tb;
+        w.b = w.unit / upb;
+        return w;
     }
-    bool used = true;
-    for (int j = i; j >= 0 && used;) {
-        const int p = par[j];
-        if (p >= j) set_error(a.err, SPA_DEVERR_BAD_INDEX);
-        if (p >= j || p < -1) used = false;
-        j = p;
-    }
-    const size_t base = ((size_t)b * a.Hkv + g) * a.T;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    auto fold = [&](int key) {          // one key per thread, -1: none
-        __syncthreads();
-        key_s[tid] = key;
-        float x = -INFINITY;
-        if (key >= 0) {
-            float dot = 0.f;
-            for (int c = 0; c < D; ++c) dot = fmaf(qs[c], __bfloat162float(kc[(base + key) * D + c]), dot);
-            x = dot * a.scale;
+    int before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int b = b0 + lane;
+        const int tb = b < a.B ? tiles_of(a, b) : 0;
+        int inc = tb * upb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
-        float mx = x;
-        for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        if (!(tid & 31)) red[tid >> 5] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float mn = fmaxf(m, mx);
-        const float f = mn == -INFINITY ? 1.f : expf(m - mn);
-        ps[tid] = key >= 0 ? expf(x - mn) : 0.f;
-        __syncthreads();
-        l *= f;
-        o *= f;
-        for (int u = 0; u < 128; ++u)
-            if (key_s[u] >= 0) {
-                l += ps[u];
-                if (tid < D) o = fmaf(ps[u], __bfloat162float(vc[(base + key_s[u]) * D + tid]), o);
+        const unsigned hit = __ballot_sync(0xffffffffu, b < a.B && before + inc > pos);
+        if (hit) {                        // always: pos < run_total
+            const int src = __ffs(hit) - 1;
+            const int tbs = __shfl_sync(0xffffffffu, tb, src);
+            const int base = before + __shfl_sync(0xffffffffu, inc, src) - tbs * upb;
+            w.b = b0 + src;
+            const int k = (pos - base) / tbs;
+            w.unit = w.b * upb + k;
+            w.t = pos - base - k * tbs;
+            return w;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// First entry of an ascending list that is >= j: 32 probes a step.
+__device__ __forceinline__ int lower_bound(const int32_t *list, int cnt, int j) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = cnt;                       // the answer lies in [lo, hi]
+    while (hi - lo > 0) {
+        const int step = (hi - lo + 31) / 32;
+        const int p = lo + (lane + 1) * step - 1;
+        const bool less = p < hi && __ldg(list + p) < j;
+        const int k = __popc(__ballot_sync(0xffffffffu, less));
+        const int nlo = min(hi, lo + k * step);
+        hi = min(hi, lo + (k + 1) * step - 1);
+        lo = nlo;
+        if (hi < lo) hi = lo;
+    }
+    return lo;
+}
+
+template <int D, int BLK, int RT>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, TreeArgs a) {
+    using C = Cfg<D, BLK, RT>;
+    constexpr int PER = C::PER, NK = C::NK, NV = C::NV;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint32_t *ulist = reinterpret_cast<uint32_t *>(smem + C::OFF_LIST);
+    uint16_t *mark = reinterpret_cast<uint16_t *>(smem + C::OFF_MARK);
+    __shared__ uint64_t bar_q, full_k[NK], empty_k[NK], full_v[NV], empty_v[NV], s_full[2],
+        p_ready[2], o_done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int sh_b, sh_unit, sh_t;
+    __shared__ int sh_total;
+    __shared__ int par[kTile];
+    __shared__ uint32_t nmask[kTile][4];          // ancestors and self; all zero: unused
+    __shared__ int wcount[kThreads / 32];
+    __shared__ int lo_s[16], hi_s[16];
+    __shared__ float st_m[2][kTile], st_l[2][kTile];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&bar_q, 1);
+        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 1); mbar_init(&empty_k[s], 1); }
+        for (int s = 0; s < NV; ++s) { mbar_init(&full_v[s], 1); mbar_init(&empty_v[s], 1); }
+        for (int w = 0; w < 2; ++w) { mbar_init(&s_full[w], 1); mbar_init(&p_ready[w], 128); }
+        mbar_init(&o_done, 1);
+        fence_mbar_init();
+        fence_async_shared();
+    }
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
+    if (warp == 9) tmem_alloc(&tmem_slot, 512);
+    if (warp == 1) {
+        const int t = run_total(a);
+        if (lane == 0) sh_total = t;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int chunk = run_chunk(sh_total);
+    int pos = blockIdx.x * chunk;
+    const int end = min(sh_total, pos + chunk);
+
+    bool ok = true;                    // cleared by a wait that ran out: no more work, no waits
+    int tu = 0;                        // key tiles so far (ring position)
+    int jobs_done[2] = {0, 0};         // jobs of each warpgroup so far (barrier phases)
+    int segs = 0;                      // segments so far (phases of bar_q, o_done)
+
+    for (; pos < end; ++segs) {
+        // ------------------------------------------------ the segment
+        if (warp == 0) {
+            const Where w = locate(a, pos);
+            if (lane == 0) {
+                sh_b = w.b;
+                sh_unit = w.unit;
+                sh_t = w.t;
             }
-        m = mn;
-    };
-    if (used) {
-        const int nb = (a.T + a.block - 1) / a.block;
-        const int per = 128 / a.block;
-        const size_t unit = (size_t)b * a.Hq + h;
-        int cnt = a.idx ? a.count[unit] : nb;
-        if (cnt < 0 || (a.idx && cnt > a.cap)) {
-            set_error(a.err, SPA_DEVERR_BAD_COUNT);
-            cnt = cnt < 0 ? 0 : a.cap;
         }
-        for (int e0 = 0; e0 < cnt; e0 += per) {
-            const int e = e0 + tid / a.block;
-            int j = -1;
-            if (e < cnt) {
-                j = a.idx ? a.idx[unit * a.cap + e] : e;
-                if (j < 0 || j >= nb || (a.idx && e > 0 && a.idx[unit * a.cap + e - 1] >= j)) {
+        __syncthreads();
+        const int b = sh_b, unit = sh_unit, t_lo = sh_t;
+        const int rt = unit % a.nrt, bg = unit / a.nrt, g = bg % a.Hkv;
+        const int P = text_len(a, b);
+        const int text_tiles = (P + kTile - 1) / kTile;
+        const int t_hi = min(text_tiles + 1, t_lo + (end - pos));
+        const bool whole_unit = t_lo == 0 && t_hi == text_tiles + 1;
+        const bool with_tree = t_hi == text_tiles + 1;
+        const int rows = a.G * a.n;
+        const int row0 = rt * RT * 128;              // first row of the unit in its (b, kv-head)
+        const int h_lo = row0 / a.n, h_hi = min(a.G, (min(rows, row0 + RT * 128) - 1) / a.n + 1);
+        const int nb_all = (a.T + BLK - 1) / BLK;
+        if (tid == 0 && a.lens && rt == 0 && g == 0 && with_tree) {
+            const int p = __ldg(a.lens + b);
+            if (p < 0 || p > a.T - a.n) set_error(a.err, SPA_DEVERR_BAD_COUNT);
+        }
+        if (warp == 8 && lane == 0 && ok) {
+            mbar_arrive_expect_tx(&bar_q, RT * C::SLOT);
+            const int qrow = (b * a.Hq + g * a.G) * a.n + row0;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf)
+                    tma_load_2d(smem + r * C::SLOT + hf * C::HALF, &tq, &bar_q, hf * 64, qrow + r * 128);
+        }
+        if (tid < a.n) par[tid] = __ldg(a.parents + (size_t)b * a.n + tid);
+        __syncthreads();
+        if (tid < kTile) {
+            uint32_t m0 = 0, m1 = 0, m2 = 0, m3 = 0;
+            int j = tid < a.n ? tid : -2;
+            while (j >= 0) {
+                const uint32_t bit = 1u << (j & 31);
+                if (j < 32) m0 |= bit; else if (j < 64) m1 |= bit; else if (j < 96) m2 |= bit; else m3 |= bit;
+                const int p = par[j];
+                if (p >= j) {
                     set_error(a.err, SPA_DEVERR_BAD_INDEX);
-                    j = -1;
+                    j = -2;
+                } else {
+                    j = max(p, -2);
                 }
             }
-            const int key = j * a.block + tid % a.block;
-            fold(j >= 0 && key < P ? key : -1);
+            if (j == -2) m0 = m1 = m2 = m3 = 0;
+            nmask[tid][0] = m0;
+            nmask[tid][1] = m1;
+            nmask[tid][2] = m2;
+            nmask[tid][3] = m3;
         }
-        bool see = false;
-        for (int j = i; j >= 0; j = par[j]) see = see || j == tid;
-        fold(see ? P + tid : -1);
+        __syncthreads();
+
+        // this thread's row
+        const int wg = warp >> 2;                                    // 0, 1: softmax
+        const int r = tid & 127;
+        const int row = row0 + (RT == 2 ? wg * 128 : 0) + r;         // in the (b, kv-head)
+        const int node = row % a.n, head = row / a.n;                // head: of the group
+        const bool live = wg < 2 && row < rows &&
+                          (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) != 0u;
+        const bool warp_live = __any_sync(0xffffffffu, live);
+        float m_used = -INFINITY, l = 0.f;
+        int first[2] = {1, 1};                                       // MMA: no product in O yet
+        bool any[2] = {false, false};                                // jobs of each warpgroup
+
+        const int j_lo = t_lo * PER, j_hi = min((P + BLK - 1) / BLK, t_hi * PER);
+        for (int s_lo = j_lo;; s_lo += kRange) {
+            const int s_hi = min(j_hi, s_lo + kRange);
+            const bool last = s_hi >= j_hi;
+            const int nr = max(0, s_hi - s_lo);
+            // ---------------------------------------- kept blocks of [s_lo, s_hi)
+            int nu = nr;
+            if (a.idx && nr > 0) {
+                for (int x = tid; x < (nr + 1) / 2; x += kThreads) reinterpret_cast<uint32_t *>(mark)[x] = 0u;
+                for (int hh = h_lo + warp; hh < h_hi; hh += kThreads / 32) {
+                    const size_t u = (size_t)b * a.Hq + g * a.G + hh;
+                    int cnt = __ldg(a.count + u);
+                    if (cnt < 0 || cnt > a.cap) {
+                        if (lane == 0) set_error(a.err, SPA_DEVERR_BAD_COUNT);
+                        cnt = cnt < 0 ? 0 : a.cap;
+                    }
+                    const int32_t *list = a.idx + u * a.cap;
+                    const int lo = lower_bound(list, cnt, s_lo), hi = lower_bound(list, cnt, s_hi);
+                    if (lane == 0) {
+                        lo_s[hh] = lo;
+                        hi_s[hh] = hi;
+                        if (cnt > 0 && ((last && with_tree && __ldg(list + cnt - 1) >= nb_all) ||
+                                        (s_lo == 0 && __ldg(list) < 0)))
+                            set_error(a.err, SPA_DEVERR_BAD_INDEX);
+                    }
+                }
+                __syncthreads();
+                for (int hh = h_lo; hh < h_hi; ++hh) {
+                    const int32_t *list = a.idx + ((size_t)b * a.Hq + g * a.G + hh) * a.cap;
+                    const int hi = hi_s[hh];
+#pragma unroll 4
+                    for (int p = lo_s[hh] + tid; p < hi; p += kThreads) {
+                        const int j = __ldg(list + p), before = p > 0 ? __ldg(list + p - 1) : -1;
+                        if (j < s_lo || j >= s_hi || before >= j) {
+                            set_error(a.err, SPA_DEVERR_BAD_INDEX);
+                            continue;
+                        }
+                        const int x = j - s_lo;
+                        atomicOr(reinterpret_cast<unsigned int *>(mark + (x & ~1)),
+                                 (unsigned)(1u << hh) << ((x & 1) * 16));
+                    }
+                }
+                __syncthreads();
+                // close up: each warp a stretch, behind the blocks of the warps before
+                const int steps = (nr + 31) / 32, per = (steps + kThreads / 32 - 1) / (kThreads / 32);
+                const int x_lo = min(nr, warp * per * 32), x_hi = min(nr, x_lo + per * 32);
+                int c = 0;
+                for (int x = x_lo; x < x_hi; x += 32)
+                    c += __popc(__ballot_sync(0xffffffffu, x + lane < x_hi && mark[x + lane] != 0));
+                if (lane == 0) wcount[warp] = c;
+                __syncthreads();
+                int at = 0;
+                nu = 0;
+                for (int w = 0; w < kThreads / 32; ++w) {
+                    if (w < warp) at += wcount[w];
+                    nu += wcount[w];
+                }
+                for (int x = x_lo; x < x_hi; x += 32) {
+                    const uint32_t m = x + lane < x_hi ? mark[x + lane] : 0u;
+                    const unsigned bal = __ballot_sync(0xffffffffu, m != 0);
+                    if (m) ulist[at + __popc(bal & ((1u << lane) - 1u))] = (m << 16) | (uint32_t)(x + lane);
+                    at += __popc(bal);
+                }
+                __syncthreads();
+            }
+            const int kv_tiles = (nu + PER - 1) / PER;
+            const bool tree_here = last && with_tree;
+            const int ntile = kv_tiles + (tree_here ? 1 : 0);
+            const int jobs = ntile * RT;
+            // block e of tile u: its number in the sequence and the heads that keep it
+            auto block_at = [&](int x, uint32_t &heads) -> int {
+                if (!a.idx) {
+                    heads = 0xffffu;
+                    return s_lo + x;
+                }
+                const uint32_t w = ulist[x];
+                heads = w >> 16;
+                return s_lo + (int)(w & 0xffffu);
+            };
+
+            if (warp == 8) {
+                // ------------------------------------ producer
+                if (lane == 0 && ok) {
+                    const int kv_row0 = bg * a.T;
+                    for (int u = 0; u < ntile; ++u) {
+                        const int tt = tu + u;
+                        const bool tree = tree_here && u == ntile - 1;
+                        const int nblk = tree ? (a.n + BLK - 1) / BLK : min(PER, nu - u * PER);
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const int ns = kv ? NV : NK, s = tt % ns;
+                            uint64_t *full = kv ? &full_v[s] : &full_k[s];
+                            if (!mbar_wait(kv ? &empty_v[s] : &empty_k[s], ((tt / ns) & 1) ^ 1, a.err)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(full, (uint32_t)(nblk * BLK * D * 2));
+                            unsigned char *dst = smem + (kv ? C::OFF_V : C::OFF_K) + s * C::SLOT;
+                            for (int e = 0; e < nblk; ++e) {
+                                uint32_t hm;
+                                const int rw = tree ? P + e * BLK : block_at(u * PER + e, hm) * BLK;
+#pragma unroll
+                                for (int hf = 0; hf < C::HALVES; ++hf)
+                                    tma_load_2d(dst + hf * C::HALF + e * BLK * 128, kv ? &tv : &tk, full,
+                                                hf * 64, kv_row0 + rw);
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                }
+            } else if (warp == 9) {
+                // ------------------------------------ products
+                if (lane == 0 && ok) {
+                    if (s_lo == j_lo) ok = mbar_wait(&bar_q, segs & 1, a.err);
+                    auto issue_s = [&](int m) -> bool {
+                        const int u = tu + m / RT, w = m & 1, s = u % NK;
+                        if (!mbar_wait(&full_k[s], (u / NK) & 1, a.err)) return false;
+                        tc_fence_after();
+                        const uint32_t qb = smem_u32(smem + (RT == 2 ? w * C::SLOT : 0));
+                        const uint32_t kb = smem_u32(smem + C::OFF_K + s * C::SLOT);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
+                            tc_mma_ss(tmem + w * 256, sw128_desc(qb + off, 16, 1024),
+                                      sw128_desc(kb + off, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit(&s_full[w]);
+                        if (RT == 1 || w == 1) tc_commit(&empty_k[s]);
+                        return true;
+                    };
+                    for (int m = 0; m < 2 && m < jobs && ok; ++m) ok = issue_s(m);
+                    for (int m = 0; m < jobs && ok; ++m) {
+                        const int u = tu + m / RT, w = m & 1, s = u % NV;
+                        ok = mbar_wait(&p_ready[w], (jobs_done[w] + m / 2) & 1, a.err) &&
+                             mbar_wait(&full_v[s], (u / NV) & 1, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t vb = smem_u32(smem + C::OFF_V + s * C::SLOT);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            tc_mma_ts(tmem + w * 256 + 128, tmem + w * 256 + kk * 8,
+                                      sw128_desc(vb + kk * 2048, C::HALF, 1024), C::IDESC_O,
+                                      (first[w] && kk == 0) ? 0u : 1u);
+                        first[w] = 0;
+                        if (RT == 1 || w == 1) tc_commit(&empty_v[s]);
+                        if (m + 2 < jobs) ok = issue_s(m + 2);
+                    }
+                    if (last && ok) tc_commit(&o_done);
+                }
+            } else {
+                // ------------------------------------ softmax
+                const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+                const uint32_t t_s = tmem + wg * 256 + lane_off, t_o = t_s + 128;
+                for (int m = wg; m < jobs && ok; m += 2) {
+                    const int u = m / RT;
+                    // (votes: a warp gives up as one)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[wg], (jobs_done[wg] + m / 2) & 1, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const bool tree = tree_here && u == ntile - 1;
+                    // rows of V that no key of this sequence fills (behind the text, blocks
+                    // that are not there, unused nodes) are made zero: their weight is
+                    // zero, but 0 x NaN is not
+                    bool dirty = tree;
+                    uint32_t see[4];                 // keys of the tile that this row attends to
+                    if (tree) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) see[c] = live ? nmask[node][c] : 0u;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) see[c] = 0u;
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) {
+                            if (u * PER + e >= nu) {
+                                dirty = true;
+                                continue;
+                            }
+                            uint32_t hm;
+                            const int lim = P - block_at(u * PER + e, hm) * BLK;
+                            dirty = dirty || lim < BLK;
+                            if (!live || !((hm >> head) & 1u)) continue;
+                            if constexpr (BLK == 16) {
+                                see[e / 2] |= (lim >= 16 ? 0xffffu : (1u << max(lim, 0)) - 1u) << (e % 2 * 16);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < BLK / 32; ++c) {
+                                    const int k = lim - c * 32;
+                                    see[e * (BLK / 32) + c] = k >= 32 ? 0xffffffffu : (1u << max(k, 0)) - 1u;
+                                }
+                            }
+                        }
+                    }
+                    if (dirty) {
+                        bool fill;
+                        if (tree) {
+                            fill = (nmask[r][0] | nmask[r][1] | nmask[r][2] | nmask[r][3]) == 0u;
+                        } else {
+                            const int x = u * PER + r / BLK;
+                            uint32_t hm;
+                            fill = x >= nu || block_at(x, hm) * BLK + r % BLK >= P;
+                        }
+                        const int tt = tu + u, s = tt % NV;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&full_v[s], (tt / NV) & 1, a.err));
+                        if (!ok) break;
+                        if (fill) {
+                            unsigned char *vr = smem + C::OFF_V + s * C::SLOT + r * 128;
+#pragma unroll
+                            for (int hf = 0; hf < C::HALVES; ++hf)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(vr + hf * C::HALF + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                    }
+                    if (warp_live) {
+                        float x[kTile];
+#pragma unroll
+                        for (int c = 0; c < kTile / 32; ++c) tmem_ld32f(t_s + c * 32, x + c * 32);
+                        tc_wait_ld();
+                        if ((see[0] & see[1] & see[2] & see[3]) != 0xffffffffu) {
+#pragma unroll
+                            for (int c = 0; c < kTile; ++c)
+                                x[c] = (see[c >> 5] >> (c & 31)) & 1u ? x[c] : -INFINITY;
+                        }
+                        float mp[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mp[e] = fmaxf(x[e], x[e + 8]);
+#pragma unroll
+                        for (int c = 16; c < kTile; c += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) mp[e] = fmax3(mp[e], x[c + e], x[c + 8 + e]);
+                        const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]),
+                                               fmaxf(mp[6], mp[7])) * a.scale_log2;
+                        float alpha = 1.f;
+                        bool rescale = false;
+                        if (mx > m_used + kRescaleThreshold) {
+                            alpha = fast_exp2(m_used - mx);
+                            rescale = l > 0.f;
+                            m_used = mx;
+                        }
+                        const float base = m_used == -INFINITY ? 0.f : m_used;
+                        // this warpgroup's previous P V completed before S(m) did: O is stable
+                        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o0[32];
+                                tmem_ld32(t_o + c * 32, o0);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o0[e] = __float_as_uint(__uint_as_float(o0[e]) * alpha);
+                                tmem_st32(t_o + c * 32, o0);
+                            }
+                        }
+                        uint64_t sp[4] = {0ull, 0ull, 0ull, 0ull};
+                        const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+                        const uint64_t nbase2 = f32x2(-base, -base);
+#pragma unroll
+                        for (int c = 0; c < kTile / 32; ++c) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float y0, y1;
+                                f32x2_split(fma_f32x2(f32x2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]),
+                                                      scale2, nbase2), y0, y1);
+                                const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                                sp[e & 3] = add_f32x2(sp[e & 3], f32x2(p0, p1));
+                                w[e] = pack_bf16x2(p0, p1);     // P to bf16 for the tensor cores
+                            }
+                            tmem_st16(t_s + c * 16, w);
+                        }
+                        float rs0, rs1;
+                        f32x2_split(add_f32x2(add_f32x2(sp[0], sp[1]), add_f32x2(sp[2], sp[3])), rs0, rs1);
+                        l = l * alpha + (rs0 + rs1);
+                        tc_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&p_ready[wg]);
+                }
+            }
+            any[0] = any[0] || jobs > 0;
+            any[1] = any[1] || jobs > 1;
+            tu += ntile;
+            jobs_done[0] += (jobs + 1) / 2;
+            jobs_done[1] += jobs / 2;
+            __syncthreads();
+            if (last) break;
+        }
+
+        // ------------------------------------------------ the segment's state
+        if (wg < 2) {
+            st_m[wg][r] = m_used;
+            st_l[wg][r] = l;
+            named_bar_sync(1, 256);
+            if (ok) ok = mbar_wait(&o_done, segs & 1, a.err);
+            tc_fence_after();
+            // RT = 1: both warpgroups hold a state of every row; each joins half of the
+            // columns. RT = 2: the row's only state.
+            float m_all = m_used, f0 = 1.f, f1 = 0.f, l_all = l;
+            if (RT == 1) {
+                m_all = fmaxf(st_m[0][r], st_m[1][r]);
+                const float mb = m_all == -INFINITY ? 0.f : m_all;
+                f0 = fast_exp2(st_m[0][r] - mb);
+                f1 = fast_exp2(st_m[1][r] - mb);
+                l_all = st_l[0][r] * f0 + st_l[1][r] * f1;
+            }
+            const bool use0 = RT == 2 ? any[wg] && l > 0.f : any[0] && st_l[0][r] > 0.f;
+            const bool use1 = RT == 1 && any[1] && st_l[1][r] > 0.f;
+            constexpr int COLS = RT == 1 ? D / 2 : D;
+            const int c_lo = RT == 1 ? wg * COLS : 0;
+            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t t_o0 = tmem + (RT == 2 ? wg * 256 : 0) + 128 + lane_off;
+            const uint32_t t_o1 = tmem + 256 + 128 + lane_off;
+            const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
+            const bool store = row < rows;
+            const size_t orow = ((size_t)b * a.Hq + g * a.G) * a.n + row;
+            const size_t slot = (size_t)blockIdx.x + unit;       // of this run's state of this unit
+            const int srow = row - row0;
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 32) {
+                float o[32];
+                uint32_t v[32];
+                tmem_ld32(t_o0 + c_lo + c, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = ok && use0 ? __uint_as_float(v[e]) * f0 : 0.f;
+                if (RT == 1) {
+                    tmem_ld32(t_o1 + c_lo + c, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] += ok && use1 ? __uint_as_float(v[e]) * f1 : 0.f;
+                }
+                if (!store) continue;
+                if (whole_unit) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c_lo + c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        dst[e / 8] = make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
+                                                pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                                pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (slot * RT * 128 + srow) * D + c_lo + c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            if (store && (RT == 2 || wg == 0)) {
+                if (whole_unit) {
+                    if (a.lse) a.lse[orow] = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+                } else {
+                    float *ml = a.ws_ml + (slot * RT * 128 + srow) * 2;
+                    ml[0] = m_all;
+                    ml[1] = l_all;
+                }
+            }
+            tc_fence_before();
+        }
+        __syncthreads();
+        tc_fence_after();
+        pos += t_hi - t_lo;
     }
-    if (tid < D)
-        static_cast<__nv_bfloat16 *>(a.out)[row * D + tid] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-    if (a.lse && tid == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    // copies still in flight on a failure path land before the CTA leaves
+    if (warp == 8 && lane == 0) {
+        if (segs > 0) mbar_drain(&bar_q, (segs - 1) & 1);
+        if (!ok) {
+            drain_ring<NK>(full_k, tu);
+            drain_ring<NV>(full_v, tu);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the states of the units that lie in several runs: one warp per row.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long orow = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (orow >= (long long)a.B * a.Hq * a.n) return;
+    const int rows = a.G * a.n, bg = (int)(orow / rows), row = (int)(orow - (long long)bg * rows);
+    const int b = bg / a.Hkv, unit = bg * a.nrt + row / (RT * 128);
+    const int chunk = run_chunk(run_total(a));
+    int before = 0;
+    const int tb = tiles_of(a, b);
+    if (a.lens) {
+        for (int x = lane; x < b; x += 32) before += tiles_of(a, x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    } else {
+        before = b * tb;
+    }
+    const int p0 = before * a.Hkv * a.nrt + (unit - b * a.Hkv * a.nrt) * tb;
+    const int c0 = p0 / chunk, c1 = (p0 + tb - 1) / chunk;
+    if (c0 == c1) return;                       // written by its run
+    const size_t srow = row % (RT * 128);
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml);
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, ml[((size_t)c + unit) * RT * 128 + srow].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mb = M == -INFINITY ? 0.f : M;
+    constexpr int V = D / 32;
+    float L = 0.f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const size_t at = ((size_t)c + unit) * RT * 128 + srow;
+        const float2 s = ml[at];
+        const float f = fast_exp2(s.x - mb);
+        L += s.y * f;
+        const float *src = a.ws_o + at * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] += src[e] * f;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + orow * D + lane * V);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+bool make_map(CUtensorMap *map, const void *base, uint64_t rows, int d, int box_rows) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int BLK, int RT>
+cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
+    using C = Cfg<D, BLK, RT>;
+    CUtensorMap mq, mk, mv;
+    const uint64_t kv_rows = (uint64_t)c.B * c.Hkv * c.T;
+    if (!make_map(&mq, c.q, (uint64_t)c.B * c.Hq * c.n, D, 128) || !make_map(&mk, c.kc, kv_rows, D, BLK) ||
+        !make_map(&mv, c.vc, kv_rows, D, BLK))
+        return cudaErrorNotSupported;
+    auto kern = tree_kernel<D, BLK, RT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than runs of kMinTiles tiles (the most that the lengths allow)
+    const long long most = (long long)c.B * c.Hkv * a.nrt * ((c.T - c.n + kTile - 1) / kTile + 1);
+    const long long ctas = (most + kMinTiles - 1) / kMinTiles;
+    kern<<<(unsigned)(ctas < kCtas ? ctas : kCtas), kThreads, C::SMEM, s>>>(mq, mk, mv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)c.B * c.Hq * c.n + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, RT>, a);
+}
+
+template <int D, int RT>
+cudaError_t launch_d(const TreeCall &c, const TreeArgs &a, cudaStream_t s) {
+    switch (c.block) {
+        case 16: return launch_cfg<D, 16, RT>(c, a, s);
+        case 32: return launch_cfg<D, 32, RT>(c, a, s);
+        case 64: return launch_cfg<D, 64, RT>(c, a, s);
+        default: return launch_cfg<D, 128, RT>(c, a, s);
+    }
+}
+
+// Rows that a CTA handles: 128, or 256 where there are more.
+int row_tiles(int G, int n, int &per) {
+    per = G * n > 128 ? 256 : 128;
+    return (G * n + per - 1) / per;
+}
+size_t state_rows(int B, int Hq, int Hkv, int n) {
+    int per;
+    const int nrt = row_tiles(Hq / Hkv, n, per);
+    return ((size_t)kCtas + (size_t)B * Hkv * nrt) * per;
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(int, int, int, int, int, int, int) { return 16; }
+// One state per run and unit it touches: (O, m, l) of its rows.
+size_t tree_workspace_bytes(int B, int Hq, int Hkv, int n, int, int d, int) {
+    return state_rows(B, Hq, Hkv, n) * (size_t)(d + 2) * sizeof(float);
+}
 
 cudaError_t launch_tree(const TreeCall &c, cudaStream_t s) {
-    const dim3 grid((unsigned)c.n, (unsigned)c.Hq, (unsigned)c.B);
-    if (c.d == 64)
-        tree_kernel<64><<<grid, 128, 0, s>>>(c);
-    else
-        tree_kernel<128><<<grid, 128, 0, s>>>(c);
-    return cudaGetLastError();
+    TreeArgs a;
+    a.parents = c.parents; a.lens = c.lens; a.idx = c.idx; a.count = c.count;
+    a.out = static_cast<__nv_bfloat16 *>(c.out);
+    a.lse = c.lse;
+    a.ws_o = static_cast<float *>(c.workspace);
+    a.ws_ml = a.ws_o + state_rows(c.B, c.Hq, c.Hkv, c.n) * c.d;
+    a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.n = c.n; a.T = c.T; a.cap = c.cap;
+    int per;
+    a.nrt = row_tiles(a.G, a.n, per);
+    a.scale_log2 = c.scale * kLog2e;
+    a.err = c.err;
+    if (c.d == 64) return per == 256 ? launch_d<64, 2>(c, a, s) : launch_d<64, 1>(c, a, s);
+    return per == 256 ? launch_d<128, 2>(c, a, s) : launch_d<128, 1>(c, a, s);
 }
 
 }  // namespace spa
