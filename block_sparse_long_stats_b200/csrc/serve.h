@@ -54,7 +54,7 @@ struct WeightCall {
     float *out;
     int *err;
 };
-size_t weight_workspace_bytes(int B, int Hq, int Lq, int T, int block);
+size_t weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block);
 cudaError_t launch_weight(const WeightCall &c, cudaStream_t s);
 
 cudaError_t launch_evict_select(const float *score, const int32_t *lens, int B, int Hkv, int T,

@@ -202,9 +202,9 @@ SPA_API spa_status spa_sparse_attn_tree(const void *q, const void *kc, const voi
     return launched(launch_tree(c, static_cast<cudaStream_t>(stream)), "tree attention launch");
 }
 
-SPA_API size_t spa_attn_weight_workspace_bytes(int B, int Hq, int Lq, int T, int block) {
-    if (B <= 0 || Hq <= 0 || Lq <= 0 || T < Lq || !block_ok(block)) return 0;
-    return weight_workspace_bytes(B, Hq, Lq, T, block);
+SPA_API size_t spa_attn_weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block) {
+    if (B <= 0 || Hkv <= 0 || Lq <= 0 || T < Lq || (block != 0 && !block_ok(block))) return 0;
+    return weight_workspace_bytes(B, Hkv, Lq, T, block);
 }
 
 SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, int B, int Hq,
@@ -214,7 +214,7 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
                                    float decay, void *workspace, size_t workspace_bytes,
                                    float *out, spa_stream stream) {
     record_last_error("");
-    if (!q || !k || !lse || !out) return fail(SPA_ERR_INVALID, "null pointer");
+    if (!q || !k || !lse || !workspace || !out) return fail(SPA_ERR_INVALID, "null pointer");
     if (!idx != !count) return fail(SPA_ERR_INVALID, "idx and count go together");
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || T <= 0 || d <= 0)
         return fail(SPA_ERR_INVALID, "sizes must be positive");
@@ -222,7 +222,8 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
     if (Lq > T) return fail(SPA_ERR_INVALID, "the queries are the sequence's last: Lq must be <= T");
     if (!(scale > 0.f) || !isfinite(scale)) return fail(SPA_ERR_INVALID, "scale must be > 0");
     if (!isfinite(decay)) return fail(SPA_ERR_INVALID, "decay must be finite");
-    if (!aligned16(q) || !aligned16(k) || !aligned16(lse) || !aligned16(prev) || !aligned16(out))
+    if (!aligned16(q) || !aligned16(k) || !aligned16(lse) || !aligned16(prev) || !aligned16(out) ||
+        !aligned16(workspace))
         return fail(SPA_ERR_INVALID, "tensors must be 16-byte aligned");
     if (dt != SPA_BF16) return fail(SPA_ERR_UNSUPPORTED, "the accumulated weight is bf16 only");
     if (d != 64 && d != 128) return fail(SPA_ERR_UNSUPPORTED, "d must be 64 or 128");
@@ -234,9 +235,9 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
         if (!block_ok(block)) return fail(SPA_ERR_UNSUPPORTED, "block must be 16, 32, 64 or 128");
         if (cap < (T + block - 1) / block) return fail(SPA_ERR_INVALID, "cap must be >= nb");
         if (lens && Lq != 1) return fail(SPA_ERR_INVALID, "lists of several queries need lens = NULL");
-        if (!workspace || !aligned16(workspace) || workspace_bytes < weight_workspace_bytes(B, Hq, Lq, T, block))
-            return fail(SPA_ERR_INVALID, "workspace smaller than spa_attn_weight_workspace_bytes");
     }
+    if (workspace_bytes < weight_workspace_bytes(B, Hkv, Lq, T, idx ? block : 0))
+        return fail(SPA_ERR_INVALID, "workspace smaller than spa_attn_weight_workspace_bytes");
     int *err = device_error_word();
     if (!err) return fail(SPA_ERR_CUDA, "device error word unavailable");
     const WeightCall c{q, k, B, Hq, Hkv, Lq, T, d, idx ? block : 128, cap, lse, lens, idx, count,

@@ -1,5 +1,25 @@
-// Attention weight that every cached key receives, summed over queries and the query
-// heads of its kv-head. One thread per key.
+// Attention weight that every cached key receives (bf16), on the sm_100a tensor cores.
+//
+//   w_t = sum_c exp(s q_c.k_t - lse_c) over the queries c of the key's kv-head that see t
+//
+// The score tile is taken transposed, S^T = K Q^T: 128 keys are the rows (TMEM lanes)
+// and up to 128 queries the columns, so a thread owns one key and its sum runs over its
+// own registers, with no reduction between threads. The log-sum-exp is an input, so
+// one pass over K is enough. Decode (a few queries) is bound by reading K once (256
+// bytes per key at d = 128); with some hundred queries and more the exponentials bound it
+// (16 a cycle and SM).
+//
+// A query tile holds `pc` positions of all G heads of the group (so that a causal
+// border cuts few tiles). Work is counted in (key tile, query tile) pairs, key tiles
+// outside; tiles the causal border leaves nothing of are not counted. The pairs of all
+// (b, kv-head) are cut into equal runs, one per CTA and SM. A key tile whose pairs lie in
+// several runs leaves a partial sum per run in the workspace (at most the first and the last
+// tile of a run do), and a second kernel adds them in order: no atomics, so a call repeats
+// bit for bit.
+//
+// Warp roles: warps 0-15: four warpgroups that take the pairs in turn, each with a score
+// tile of its own in tensor memory; warp 16: TMA producer; warp 17: TMEM allocator and
+// tcgen05.mma issuer.
 #include <math.h>
 
 #include "serve.h"
@@ -7,69 +27,653 @@
 namespace spa {
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) weight_kernel(WeightCall a) {
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
-    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k);
-    const int t = blockIdx.x * 128 + threadIdx.x, bg = blockIdx.y;
-    if (t >= a.T) return;
-    const int b = bg / a.Hkv, g = bg % a.Hkv, G = a.Hq / a.Hkv;
-    int len = a.lens ? a.lens[b] : a.T;
-    if (len < a.Lq || len > a.T) {
-        set_error(a.err, SPA_DEVERR_BAD_COUNT);
-        len = len < a.Lq ? a.Lq : a.T;
+constexpr int kCtas = 148;             // one per SM
+constexpr int kGroups = 4;             // consumer warpgroups
+constexpr int kConsumers = kGroups * 128;
+constexpr int kThreads = kConsumers + 64;
+constexpr int kTile = 128;             // keys
+constexpr int kMarkChunk = 2048;       // blocks per CTA of the mark kernel
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct WeightArgs {
+    const int32_t *lens;
+    const float *lse, *prev;
+    const uint16_t *marks;             // [B, Hkv, nq, nbp] head masks of the kept blocks, or null
+    float *out, *parts;                // parts [2 kCtas][kTile]
+    int B, Hq, Hkv, G, Lq, T, block, nq, nbp;
+    int pc, nqt;                       // positions per query tile, query tiles
+    float scale_log2, decay;
+    int *err;
+};
+
+template <int D, int NC, bool STREAM>
+struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int K_HALF = kTile * 128;
+    static constexpr int K_SLOT = HALVES * K_HALF;
+    static constexpr int Q_HALF = NC * 128;
+    static constexpr int Q_SLOT = HALVES * Q_HALF;
+    // streams of query tiles want a deep query ring, a stream of key tiles a deep key ring
+    static constexpr int NK = STREAM ? 2 : (D == 64 ? 8 : 4);
+    static constexpr int NQ = STREAM ? 4 : 2;
+    static constexpr int OFF_Q = NK * K_SLOT;
+    static constexpr int SMEM = OFF_Q + NQ * Q_SLOT + 1024;
+    static constexpr uint32_t IDESC = idesc_bf16(128, NC, false);
+};
+
+__device__ __forceinline__ int seq_len(const WeightArgs &a, int b) {
+    const int n = a.lens ? __ldg(a.lens + b) : a.T;
+    return min(max(n, a.Lq), a.T);
+}
+// First query tile that sees key tile kt (off: position of the first query).
+__device__ __forceinline__ int first_tile(const WeightArgs &a, int kt, int off) {
+    const int t0 = kt * kTile - off;
+    return t0 > 0 ? t0 / a.pc : 0;
+}
+// Pairs of one (b, kv-head), summed by a warp.
+__device__ __forceinline__ long long pairs_of(const WeightArgs &a, int b) {
+    const int len = seq_len(a, b), nt = (len + kTile - 1) / kTile, off = len - a.Lq;
+    long long s = (long long)nt * a.nqt;
+    if (a.nqt == 1) return s;
+    long long skip = 0;
+    for (int kt = max(0, off / kTile) + (int)(threadIdx.x & 31); kt < nt; kt += 32) skip += first_tile(a, kt, off);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) skip += __shfl_xor_sync(0xffffffffu, skip, o);
+    return s - skip;
+}
+__device__ __forceinline__ long long run_total(const WeightArgs &a) {
+    if (!a.lens) return (long long)a.B * a.Hkv * pairs_of(a, 0);
+    long long s = 0;
+    if (a.nqt == 1) {
+        for (int b = threadIdx.x & 31; b < a.B; b += 32) s += (seq_len(a, b) + kTile - 1) / kTile;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    } else {
+        for (int b = 0; b < a.B; ++b) s += pairs_of(a, b);
     }
-    const __nv_bfloat16 *kr = k + ((size_t)bg * a.T + t) * D;
-    const int q0 = (len - a.Lq) / a.block, nq = (len - 1) / a.block - q0 + 1;
-    float sum = 0.f;
-    for (int h = g * G; h < g * G + G && t < len; ++h)
-        for (int qb = 0; qb < nq; ++qb) {
-            const size_t unit = ((size_t)b * a.Hq + h) * nq + qb;
-            bool kept = true;
-            if (a.idx) {
-                int cnt = a.count[unit], last = -1;
-                if (cnt < 0 || cnt > a.cap) {
-                    set_error(a.err, SPA_DEVERR_BAD_COUNT);
-                    cnt = cnt < 0 ? 0 : a.cap;
-                }
-                kept = false;
-                for (int e = 0; e < cnt; ++e) {
-                    const int j = a.idx[unit * a.cap + e];
-                    if (j <= last || j > (a.T - 1) / a.block) {
-                        set_error(a.err, SPA_DEVERR_BAD_INDEX);
-                        continue;
-                    }
-                    last = j;
-                    kept = kept || j == t / a.block;
+    return s * a.Hkv;
+}
+__device__ __forceinline__ long long run_chunk(long long total) {
+    const long long c = (total + kCtas - 1) / kCtas;
+    return c < 1 ? 1 : c;
+}
+
+// A pair: sequence and kv-head, key tile, query tile. Advances in the runs' order.
+struct Pair {
+    int b, bg, kt, qi, nt, off;
+    __device__ void at_head(const WeightArgs &a) {
+        const int len = seq_len(a, b);
+        nt = (len + kTile - 1) / kTile;
+        off = len - a.Lq;
+    }
+    // Returns whether the key tile changed; new_head whether the (b, kv-head) did.
+    __device__ bool next(const WeightArgs &a, bool &new_head) {
+        new_head = false;
+        if (++qi < a.nqt) return false;
+        if (++kt >= nt) {
+            kt = 0;
+            ++bg;
+            new_head = true;
+            if (bg % a.Hkv == 0 && ++b < a.B) at_head(a);
+        }
+        qi = first_tile(a, kt, off);
+        return true;
+    }
+};
+
+// The pair at position pos of the runs; every lane of a warp calls it together.
+__device__ __forceinline__ Pair locate(const WeightArgs &a, long long pos) {
+    const int lane = threadIdx.x & 31;
+    Pair p;
+    p.b = 0;
+    long long per = 0;
+    if (!a.lens) {
+        per = pairs_of(a, 0);
+        p.bg = (int)(pos / per);
+        p.b = p.bg / a.Hkv;
+        pos -= per * p.bg;
+    } else {
+        for (;; ++p.b) {
+            per = pairs_of(a, p.b);
+            if (pos < per * a.Hkv || p.b + 1 >= a.B) break;
+            pos -= per * a.Hkv;
+        }
+        const int g = (int)(pos / per);
+        p.bg = p.b * a.Hkv + g;
+        pos -= per * g;
+    }
+    p.at_head(a);
+    if (a.nqt == 1) {
+        p.kt = (int)pos;
+        p.qi = 0;
+        return p;
+    }
+    for (int k0 = 0;; k0 += 32) {                  // 32 key tiles a step
+        const int kt = k0 + lane;
+        const int np = kt < p.nt ? a.nqt - first_tile(a, kt, p.off) : 0;
+        long long inc = np;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > pos);
+        if (hit || k0 + 32 >= p.nt) {
+            const int src = hit ? __ffs(hit) - 1 : 0;
+            p.kt = k0 + src;
+            const long long rest = pos - (__shfl_sync(0xffffffffu, inc, src) - __shfl_sync(0xffffffffu, np, src));
+            p.qi = first_tile(a, p.kt, p.off) + (int)rest;
+            return p;
+        }
+        pos -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// Sets bits [lo, hi) of a 128-bit mask.
+__device__ __forceinline__ void set_range(uint32_t (&m)[4], int lo, int hi) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
+        const uint32_t below_h = h == 32 ? 0xffffffffu : (1u << h) - 1u;
+        const uint32_t below_l = l == 32 ? 0xffffffffu : (1u << l) - 1u;
+        m[w] |= below_h & ~below_l;
+    }
+}
+
+template <int D, int NC, bool STREAM>
+__global__ void __launch_bounds__(kThreads, 1)
+    weight_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  WeightArgs a) {
+    using C = Cfg<D, NC, STREAM>;
+    constexpr int NK = C::NK, NQ = C::NQ;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full_k[NK], empty_k[NK], full_q[NQ], empty_q[NQ], s_full[kGroups], s_empty[kGroups];
+    __shared__ uint32_t tmem_slot;
+    __shared__ Pair sh_pair;
+    __shared__ long long sh_total;
+    __shared__ __align__(16) float nl_s[kGroups][NC];   // -lse of the columns, log2 units
+    __shared__ float red[2][kGroups][kTile];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 1); mbar_init(&empty_k[s], 1); }
+        for (int s = 0; s < NQ; ++s) { mbar_init(&full_q[s], 1); mbar_init(&empty_q[s], 1); }
+        for (int w = 0; w < kGroups; ++w) { mbar_init(&s_full[w], 1); mbar_init(&s_empty[w], 128); }
+        fence_mbar_init();
+    }
+    // query rows that no copy fills stay zero (finite scores; their columns count nothing)
+    for (int x = tid; x < NQ * C::Q_SLOT / 16; x += kThreads)
+        reinterpret_cast<uint4 *>(smem + C::OFF_Q)[x] = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+    if (warp == 16 && lane == 0) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+    }
+    if (warp == 17) tmem_alloc(&tmem_slot, 512);
+    if (warp == 0) {
+        const long long t = run_total(a), pos = (long long)blockIdx.x * run_chunk(t);
+        if (lane == 0) sh_total = t;
+        if (pos < t) {
+            const Pair p = locate(a, pos);
+            if (lane == 0) sh_pair = p;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (a.marks) asm volatile("griddepcontrol.wait;" ::: "memory");   // the mark kernel's output
+    const uint32_t tmem = tmem_slot;
+    const long long chunk = run_chunk(sh_total), pos0 = (long long)blockIdx.x * chunk;
+    const long long jobs = max(0ll, min(sh_total, pos0 + chunk) - pos0);
+    const bool gq1 = a.nq == 1;
+
+    if (warp == 16) {
+        // ---------------------------------------------------- producer
+        bool ok = true;
+        int nk = 0, nqs = 0;
+        Pair p = sh_pair;
+        bool new_k = true, new_q = true;
+        int kept = 0, kept_at = -1;      // lane i: kept blocks of key tile kept_at + i
+        for (long long m = 0; m < jobs && ok; ++m) {
+            if (new_q && lane == 0) {
+                const int s = nqs % NQ;
+                ok = mbar_wait(&empty_q[s], ((nqs / NQ) & 1) ^ 1, a.err);
+                if (ok) {
+                    mbar_arrive_expect_tx(&full_q[s], (uint32_t)(a.pc * a.G * D * 2));
+                    const int head = p.b * a.Hq + (p.bg % a.Hkv) * a.G;
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                        asm volatile(
+                            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+                                smem_u32(smem + C::OFF_Q + s * C::Q_SLOT + hf * C::Q_HALF)),
+                            "l"(&tq), "r"(smem_u32(&full_q[s])), "r"(hf * 64), "r"(p.qi * a.pc), "r"(head)
+                            : "memory");
                 }
             }
-            if (!kept) continue;
-            const int i_lo = max(max((q0 + qb) * a.block, len - a.Lq), t) - (len - a.Lq);
-            const int i_hi = min((q0 + qb + 1) * a.block, len) - (len - a.Lq);
-            for (int i = i_lo; i < i_hi; ++i) {
-                const size_t row = ((size_t)b * a.Hq + h) * a.Lq + i;
-                const float ls = a.lse[row];
-                float dot = 0.f;
-                for (int c = 0; c < D; ++c)
-                    dot = fmaf(__bfloat162float(q[row * D + c]), __bfloat162float(kr[c]), dot);
-                if (ls != -INFINITY) sum += expf(dot * a.scale - ls);
+            if (new_q) ++nqs;
+            if (new_k) {
+                const int per = kTile / a.block;
+                int want = (1 << per) - 1;
+                if (a.marks && gq1) {    // one list per head: blocks that no head keeps are not read
+                    if (kept_at < 0 || p.kt >= kept_at + 32 || p.kt < kept_at || p.kt == 0) {
+                        kept_at = p.kt;
+                        kept = 0;
+                        const int kt = p.kt + lane;
+                        if (kt < p.nt)
+                            for (int e = 0; e < per; ++e) {
+                                const int j = kt * per + e;
+                                if (j < a.nbp && a.marks[(size_t)p.bg * a.nbp + j]) kept |= 1 << e;
+                            }
+                    }
+                    want = __shfl_sync(0xffffffffu, kept, p.kt - kept_at);
+                }
+                if (lane == 0 && ok) {
+                    const int s = nk % NK;
+                    ok = mbar_wait(&empty_k[s], ((nk / NK) & 1) ^ 1, a.err);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&full_k[s], (uint32_t)(__popc(want) * a.block * D * 2));
+                        for (int e = 0; e < per; ++e)
+                            if ((want >> e) & 1) {
+#pragma unroll
+                                for (int hf = 0; hf < C::HALVES; ++hf)
+                                    tma_load_2d(smem + s * C::K_SLOT + hf * C::K_HALF + e * a.block * 128, &tk,
+                                                &full_k[s], hf * 64, p.bg * a.T + p.kt * kTile + e * a.block);
+                            }
+                    }
+                }
+                ++nk;
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            bool head;
+            new_k = p.next(a, head);
+            new_q = STREAM || head;
+        }
+        if (lane == 0 && !ok) {
+            drain_ring<NK>(full_k, nk);
+            drain_ring<NQ>(full_q, nqs);
+        }
+    } else if (warp == 17) {
+        // ---------------------------------------------------- products
+        if (lane == 0) {
+            bool ok = true, new_k = true, new_q = true;
+            int nk = 0, nqs = 0;
+            Pair p = sh_pair;
+            for (long long m = 0; m < jobs && ok; ++m) {
+                const int w = (int)(m & (kGroups - 1));
+                if (new_k) { ok = mbar_wait(&full_k[nk % NK], (nk / NK) & 1, a.err); ++nk; }
+                if (new_q && ok) { ok = mbar_wait(&full_q[nqs % NQ], (nqs / NQ) & 1, a.err); }
+                if (new_q) ++nqs;
+                if (ok) ok = mbar_wait(&s_empty[w], (uint32_t)((m / kGroups) & 1) ^ 1u, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t kb = smem_u32(smem + ((nk - 1) % NK) * C::K_SLOT);
+                const uint32_t qb = smem_u32(smem + C::OFF_Q + ((nqs - 1) % NQ) * C::Q_SLOT);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_ss(tmem + w * 128, sw128_desc(kb + (kk >> 2) * C::K_HALF + (kk & 3) * 32, 16, 1024),
+                              sw128_desc(qb + (kk >> 2) * C::Q_HALF + (kk & 3) * 32, 16, 1024), C::IDESC,
+                              kk > 0 ? 1u : 0u);
+                tc_commit(&s_full[w]);
+                const int k_used = (nk - 1) % NK, q_used = (nqs - 1) % NQ;
+                bool head;
+                new_k = p.next(a, head);
+                new_q = STREAM || head;
+                if (new_k) tc_commit(&empty_k[k_used]);
+                if (new_q) tc_commit(&empty_q[q_used]);
             }
         }
-    const size_t o = (size_t)bg * a.T + t;
-    a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], sum) : sum;
+    } else {
+        // ---------------------------------------------------- sums
+        const int wg = warp >> 2, r = tid & 127;
+        const uint32_t t_s = tmem + wg * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+        const int ch = r / a.pc, ci = r - ch * a.pc;       // column r: head of the group, position
+        const bool col = r < NC && ch < a.G;
+        // keys behind every sequence: no weight
+        for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
+            const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kTile - 1) / kTile * kTile;
+            if (a.lens && tid == 0 && bg % a.Hkv == 0) {
+                const int n = __ldg(a.lens + b);
+                if (n < a.Lq || n > a.T) set_error(a.err, SPA_DEVERR_BAD_COUNT);
+            }
+            for (int t = t0 + tid; t < a.T; t += kConsumers) {
+                const size_t o = (size_t)bg * a.T + t;
+                a.out[o] = a.prev ? a.decay * a.prev[o] : 0.f;
+            }
+        }
+        Pair p = sh_pair;
+        bool ok = true, fresh = true;          // fresh: this group's columns changed
+        float sum = 0.f;
+        int units = 0;
+        long long unit_first = 0;              // the key tile's first pair in this run
+        const int first_qi = jobs > 0 ? first_tile(a, p.kt, p.off) : 0;
+        bool from_start = jobs > 0 && p.qi == first_qi;
+        for (long long m = 0; m < jobs; ++m) {
+            const bool mine = (m & (kGroups - 1)) == wg;
+            const int t = p.kt * kTile + r;
+            const size_t o = (size_t)p.bg * a.T + t;
+            const bool last_pair = p.qi == a.nqt - 1;      // of the key tile
+            if (mine) {
+                // loads that need no score: ahead of the wait
+                float nl = -INFINITY;
+                if (fresh && col && p.qi * a.pc + ci < a.Lq) {
+                    const int g = p.bg % a.Hkv;
+                    const float x = __ldg(a.lse + ((size_t)p.b * a.Hq + g * a.G + ch) * a.Lq + p.qi * a.pc + ci);
+                    nl = x == -INFINITY ? -INFINITY : -x * kLog2e;
+                }
+                float before = 0.f;
+                if (!STREAM && a.prev && t < a.T) before = a.prev[o];
+                uint32_t see[4];
+                bool masked = false;
+                const int q0 = p.off + p.qi * a.pc;        // position of the tile's first query
+                const int lim = t - q0;                    // positions from lim on see the key
+                if (a.marks) {
+                    masked = true;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) see[c] = 0u;
+                    const int blk = t / a.block, qb0 = p.off / a.block;
+                    if (t < a.T) {
+                        const uint16_t *mk = a.marks + (size_t)p.bg * a.nq * a.nbp + blk;
+                        if (!STREAM && a.pc == 1) {
+                            see[0] = mk[0];
+                        } else {
+                            const int q_end = min(a.Lq, (p.qi + 1) * a.pc) + p.off;
+                            for (int qb = q0 / a.block; qb * a.block < q_end; ++qb) {
+                                const uint32_t hm = mk[(size_t)(qb - qb0) * a.nbp];
+                                const int lo = max(max(qb * a.block - q0, 0), lim);
+                                const int hi = min((qb + 1) * a.block, q_end) - q0;
+                                if (lo < hi)
+                                    for (int h = 0; h < a.G; ++h)
+                                        if ((hm >> h) & 1u) set_range(see, h * a.pc + lo, h * a.pc + hi);
+                            }
+                        }
+                    }
+                } else if (p.kt * kTile + kTile - 1 > q0) {        // the causal border
+                    masked = true;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) see[c] = 0u;
+                    if (lim < a.pc)
+                        for (int h = 0; h < a.G; ++h) set_range(see, h * a.pc + max(lim, 0), (h + 1) * a.pc);
+                }
+                if (fresh) {
+                    named_bar_sync(2 + wg, 128);           // the group is done with the last columns
+                    if (r < NC) nl_s[wg][r] = nl;
+                    named_bar_sync(2 + wg, 128);
+                }
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[wg], (uint32_t)((m / kGroups) & 1), a.err));
+                if (ok) {
+                    tc_fence_after();
+                    uint64_t acc[2] = {0ull, 0ull};
+                    const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+                    constexpr int STEP = NC < 32 ? 16 : 32;
+#pragma unroll
+                    for (int c0 = 0; c0 < NC; c0 += STEP) {
+                        float x[32];
+                        if constexpr (STEP == 32) {
+                            tmem_ld32f(t_s + c0, x);
+                        } else {
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                                : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+                                  "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]),
+                                  "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+                                : "r"(t_s));
+                        }
+                        tc_wait_ld();
+                        const uint32_t bits = masked ? see[c0 >> 5] : 0xffffffffu;
+#pragma unroll
+                        for (int e = 0; e < STEP; e += 4) {
+                            const float4 n4 = *reinterpret_cast<const float4 *>(&nl_s[wg][c0 + e]);
+                            float y0, y1, y2, y3;
+                            f32x2_split(fma_f32x2(f32x2(x[e], x[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
+                            f32x2_split(fma_f32x2(f32x2(x[e + 2], x[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
+                            if (masked) {          // a key no one keeps may hold anything: select
+                                y0 = (bits >> e) & 1u ? y0 : -INFINITY;
+                                y1 = (bits >> (e + 1)) & 1u ? y1 : -INFINITY;
+                                y2 = (bits >> (e + 2)) & 1u ? y2 : -INFINITY;
+                                y3 = (bits >> (e + 3)) & 1u ? y3 : -INFINITY;
+                            }
+                            acc[0] = add_f32x2(acc[0], f32x2(fast_exp2(y0), fast_exp2(y1)));
+                            acc[1] = add_f32x2(acc[1], f32x2(fast_exp2(y2), fast_exp2(y3)));
+                        }
+                    }
+                    float s0, s1;
+                    f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
+                    sum += s0 + s1;
+                    tc_fence_before();
+                    mbar_arrive(&s_empty[wg]);
+                }
+                fresh = false;
+                if (!STREAM) {                              // the key tile's only pair
+                    if (t < a.T) {
+                        const bool in = t < p.off + a.Lq;
+                        a.out[o] = a.prev ? fmaf(a.decay, before, in ? sum : 0.f) : (in ? sum : 0.f);
+                    }
+                    sum = 0.f;
+                }
+            }
+            if (STREAM && (last_pair || m + 1 == jobs)) {
+                // the key tile's sum over the groups, in their order
+                red[units & 1][wg][r] = sum;
+                sum = 0.f;
+                named_bar_sync(1, kConsumers);
+                if ((units & (kGroups - 1)) == wg && t < a.T) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kGroups; ++w) s += red[units & 1][w][r];
+                    if (t >= p.off + a.Lq) s = 0.f;
+                    if (from_start && last_pair)
+                        a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
+                    else
+                        a.parts[((size_t)blockIdx.x * 2 + (unit_first > 0 ? 1 : 0)) * kTile + r] = s;
+                }
+                ++units;
+                unit_first = m + 1;
+                from_start = true;
+            }
+            bool head;
+            p.next(a, head);
+            fresh = fresh || STREAM || head;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
+
+// Adds the partial sums of the key tiles that lie in several runs: CTA c looks after the
+// tile that run c begins inside of, if that tile began in run c - 1 or before and no
+// run between begins inside of it too.
+__global__ void __launch_bounds__(kTile) weight_join_kernel(WeightArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int r = threadIdx.x;
+    const long long total = run_total(a), chunk = run_chunk(total);
+    const long long pos = (long long)blockIdx.x * chunk;
+    if (blockIdx.x == 0 || pos >= total) return;
+    const Pair p = locate(a, pos);
+    const int first = first_tile(a, p.kt, p.off);
+    if (p.qi == first) return;                                       // run c begins with a tile
+    const long long t_pos = pos - (p.qi - first), t_end = t_pos + (a.nqt - first);
+    const int c0 = (int)(t_pos / chunk), c1 = (int)((t_end - 1) / chunk);
+    if ((int)blockIdx.x != c0 + 1) return;                            // the first run that continues it
+    const int t = p.kt * kTile + r;
+    if (t >= a.T) return;
+    float s = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const bool begins = c == c0 && t_pos != (long long)c0 * chunk;
+        s += a.parts[((size_t)c * 2 + (begins ? 1 : 0)) * kTile + r];
+    }
+    const size_t o = (size_t)p.bg * a.T + t;
+    a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
+}
+
+// Head masks of the kept blocks, [B, Hkv, nq, nbp]: CTA ((b, kv-head, query block), chunk
+// of blocks).
+__global__ void __launch_bounds__(256) mark_kernel(const int32_t *__restrict__ idx, const int32_t *__restrict__ count,
+                                                   int Hkv, int G, int nq, int nb, int nbp, int cap,
+                                                   uint16_t *__restrict__ marks, int *err) {
+    __shared__ __align__(16) uint16_t mk[kMarkChunk];
+    const int unit = blockIdx.x, bg = unit / nq, qb = unit % nq, j_lo = blockIdx.y * kMarkChunk;
+    const int j_hi = min(nbp, j_lo + kMarkChunk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int x = threadIdx.x; x < kMarkChunk / 8; x += 256) reinterpret_cast<uint4 *>(mk)[x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int h = warp & 3; h < G; h += 4) {                 // two warps per head
+        const size_t u = (((size_t)bg * G) + h) * nq + qb;
+        int cnt = __ldg(count + u);
+        if (cnt < 0 || cnt > cap) {
+            set_error(err, SPA_DEVERR_BAD_COUNT);
+            cnt = cnt < 0 ? 0 : cap;
+        }
+        const int32_t *list = idx + u * cap;
+        // lists shorter than a chunk are read whole, longer ones from a 32-way search on
+        int lo = 0, hi = cnt;
+        while (hi - lo > 1024) {
+            const int step = (hi - lo + 31) / 32, q = lo + (lane + 1) * step - 1;
+            const bool less = q < hi && __ldg(list + q) < j_lo;
+            const int k = __popc(__ballot_sync(0xffffffffu, less));
+            const int nlo = min(hi, lo + k * step);
+            hi = max(nlo, min(hi, lo + (k + 1) * step - 1));
+            lo = nlo;
+        }
+        for (int e0 = lo + (warp >> 2) * 128; e0 < cnt; e0 += 256) {
+            int j[4], before[4];
+            bool past = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + i * 32 + lane;
+                j[i] = e < cnt ? __ldg(list + e) : 0x7fffffff;
+                before[i] = e < cnt && e > 0 ? __ldg(list + e - 1) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (e0 + i * 32 + lane >= cnt) continue;
+                if (j[i] < 0 || j[i] >= nb || before[i] >= j[i]) {
+                    set_error(err, SPA_DEVERR_BAD_INDEX);
+                    past = false;
+                    continue;
+                }
+                past = past && j[i] >= j_hi;
+                if (j[i] >= j_lo && j[i] < j_hi) {
+                    const int x = j[i] - j_lo;
+                    atomicOr(reinterpret_cast<unsigned int *>(mk + (x & ~1)), (unsigned)(1u << h) << ((x & 1) * 16));
+                }
+            }
+            if (__all_sync(0xffffffffu, past)) break;
+        }
+    }
+    __syncthreads();
+    uint4 *dst = reinterpret_cast<uint4 *>(marks + (size_t)unit * nbp + j_lo);
+    for (int x = threadIdx.x; x < (j_hi - j_lo) / 8; x += 256) dst[x] = reinterpret_cast<const uint4 *>(mk)[x];
+}
+
+bool make_maps(CUtensorMap *mq, CUtensorMap *mk, const WeightCall &c, int pc) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint32_t one[3] = {1, 1, 1};
+    const cuuint64_t qd[3] = {(cuuint64_t)c.d, (cuuint64_t)c.Lq, (cuuint64_t)c.B * c.Hq};
+    const cuuint64_t qs[2] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.Lq * c.d * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)pc, (cuuint32_t)(c.Hq / c.Hkv)};
+    const cuuint64_t kd[2] = {(cuuint64_t)c.d, (cuuint64_t)c.B * c.Hkv * c.T};
+    const cuuint64_t ks[1] = {(cuuint64_t)c.d * 2};
+    const cuuint32_t kb[2] = {64, (cuuint32_t)c.block};
+    return enc(mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(c.q), qd, qs, qb, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           enc(mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(c.k), kd, ks, kb, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_after(const void *kern, dim3 grid, dim3 block, size_t smem, void **args, bool overlap,
+                         cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+template <int D, int NC, bool STREAM>
+cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
+    using C = Cfg<D, NC, STREAM>;
+    CUtensorMap mq, mk;
+    if (!make_maps(&mq, &mk, c, a.pc)) return cudaErrorNotSupported;
+    const void *kern = reinterpret_cast<const void *>(weight_kernel<D, NC, STREAM>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const long long most = (long long)c.B * c.Hkv * ((c.T + kTile - 1) / kTile) * a.nqt;
+    void *args[] = {&mq, &mk, &a};
+    e = launch_after(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kThreads), C::SMEM, args,
+                     a.marks != nullptr, s);
+    if (e != cudaSuccess || !STREAM) return e;
+    void *jargs[] = {&a};
+    return launch_after(reinterpret_cast<const void *>(weight_join_kernel), dim3(kCtas), dim3(kTile), 0, jargs,
+                        true, s);
+}
+
+template <int D>
+cudaError_t launch_d(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
+    // query tiles of 128 rows, in a stream; or one tile as narrow as the rows allow
+    if (a.nqt > 1) return launch_cfg<D, 128, true>(c, a, s);
+    const int rows = a.G * a.pc;
+    if (rows <= 16) return launch_cfg<D, 16, false>(c, a, s);
+    if (rows <= 64) return launch_cfg<D, 64, false>(c, a, s);
+    return launch_cfg<D, 128, false>(c, a, s);
+}
+
+int query_blocks(int Lq, int T, int block) { return (T - 1) / block - (T - Lq) / block + 1; }
+constexpr size_t kPartBytes = (size_t)2 * kCtas * kTile * sizeof(float);
 
 }  // namespace
 
-size_t weight_workspace_bytes(int, int, int, int, int) { return 16; }
+// Partial sums of the runs, then (with lists: block > 0) the head masks.
+size_t weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block) {
+    size_t n = kPartBytes;
+    if (block > 0) {
+        const size_t nbp = ((size_t)((T + block - 1) / block) + 7) & ~size_t(7);
+        n += (size_t)B * Hkv * query_blocks(Lq, T, block) * nbp * sizeof(uint16_t);
+    }
+    return n;
+}
 
 cudaError_t launch_weight(const WeightCall &c, cudaStream_t s) {
-    const dim3 grid((unsigned)((c.T + 127) / 128), (unsigned)(c.B * c.Hkv));
-    if (c.d == 64)
-        weight_kernel<64><<<grid, 128, 0, s>>>(c);
-    else
-        weight_kernel<128><<<grid, 128, 0, s>>>(c);
-    return cudaGetLastError();
+    WeightArgs a;
+    a.lens = c.lens; a.lse = c.lse; a.prev = c.prev;
+    a.out = c.out;
+    a.parts = static_cast<float *>(c.workspace);
+    a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.Lq = c.Lq; a.T = c.T; a.block = c.block;
+    a.pc = kTile / a.G < c.Lq ? kTile / a.G : c.Lq;
+    a.nqt = (c.Lq + a.pc - 1) / a.pc;
+    a.scale_log2 = c.scale * kLog2e;
+    a.decay = c.decay;
+    a.err = c.err;
+    a.marks = nullptr;
+    a.nq = query_blocks(c.Lq, c.T, c.block);
+    a.nbp = 0;
+    if (c.idx) {
+        const int nb = (c.T + c.block - 1) / c.block;
+        a.nbp = (nb + 7) & ~7;
+        uint16_t *marks = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(c.workspace) + kPartBytes);
+        a.marks = marks;
+        const dim3 grid((unsigned)(c.B * c.Hkv * a.nq), (unsigned)((a.nbp + kMarkChunk - 1) / kMarkChunk));
+        mark_kernel<<<grid, 256, 0, s>>>(c.idx, c.count, c.Hkv, a.G, a.nq, nb, a.nbp, c.cap, marks, c.err);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return c.d == 64 ? launch_d<64>(c, a, s) : launch_d<128>(c, a, s);
 }
 
 }  // namespace spa

@@ -740,8 +740,8 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
     return out, lse
 
 
-def spa_attn_weight_workspace_bytes(B: int, Hq: int, Lq: int, T: int, block: int) -> int:
-    return int(lib().spa_attn_weight_workspace_bytes(B, Hq, Lq, T, block))
+def spa_attn_weight_workspace_bytes(B: int, Hkv: int, Lq: int, T: int, block: int) -> int:
+    return int(lib().spa_attn_weight_workspace_bytes(B, Hkv, Lq, T, block))
 
 
 def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: float,
@@ -760,14 +760,11 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
         if idx is not None or count is not None:
             nq = (T - 1) // block - (T - Lq) // block + 1 if block > 0 else 0
             ip, cap, cp = _lists(idx, count, B, Hq, nq, dev)
-            if workspace is None:
-                need = spa_attn_weight_workspace_bytes(B, Hq, Lq, T, block)
-                workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
-        wp, wn = None, 0
-        if workspace is not None:
-            if not workspace.is_contiguous() or workspace.device != dev:
-                raise ValueError("the workspace must be contiguous and on the tensors' device")
-            wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if workspace is None:
+            need = spa_attn_weight_workspace_bytes(B, Hkv, Lq, T, 0 if idx is None else block)
+            workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
             out = torch.empty((B, Hkv, T), device=dev, dtype=torch.float32)
         _check("spa_attn_weight",
@@ -775,7 +772,8 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
                                      _dt(q), B, Hq, Hkv, Lq, T, d,
                                      _arg(lse, "lse", (B, Hq, Lq), torch.float32, dev),
                                      _arg(lens, "lens", (B,), torch.int32, dev), block, ip, cap, cp, scale,
-                                     _arg(prev, "prev", (B, Hkv, T), torch.float32, dev), decay, wp, wn,
+                                     _arg(prev, "prev", (B, Hkv, T), torch.float32, dev), decay,
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                      _arg(out, "out", (B, Hkv, T), torch.float32, dev), st))
     return out
 

@@ -608,12 +608,13 @@ spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, s
  *         Lq = 1. cap >= ceil(T/block). block: 16, 32, 64 or 128 (read with lists only)
  *   prev : [B, Hkv, T] fp32 or NULL (zero);  decay : finite
  *   out  : [B, Hkv, T] fp32, may be prev
- *   workspace : >= spa_attn_weight_workspace_bytes(...) (0 without lists: may be NULL),
- *         16-byte aligned, overwritten; calls that may overlap in time need one each
+ *   workspace : >= spa_attn_weight_workspace_bytes(...) device bytes (block = 0 there:
+ *         without lists), 16-byte aligned, overwritten; calls that may overlap in time
+ *         need one each
  * Products are accumulated in fp32, weights and their sums fp32; no atomics, so calls
  * repeat bit for bit.
  */
-size_t spa_attn_weight_workspace_bytes(int B, int Hq, int Lq, int T, int block);
+size_t spa_attn_weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block);
 spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, int B, int Hq, int Hkv,
                            int Lq, int T, int d, const float *lse, const int32_t *lens, int block,
                            const int32_t *idx, int cap, const int32_t *count, float scale,
