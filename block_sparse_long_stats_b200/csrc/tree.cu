@@ -22,8 +22,9 @@
 // the same key tile, each for its own 128 rows (RT = 2). Either way one warpgroup's
 // exponentials run beside the other's products. Warp roles:
 //   warps 0-3, 4-7 : softmax; thread r of a warpgroup owns row r = TMEM lane r
-//   warp 8         : TMA producer (Q per unit; rings of K and of V tiles)
-//   warp 9         : TMEM allocator and tcgen05.mma issuer
+//   warps 8, 10    : TMA producers (Q per unit and a ring of K tiles; a ring of V tiles)
+//   warp 9         : TMEM allocator and tcgen05.mma issuer (one for both warpgroups, which
+//                    so run in turn: with one each 10 % slower)
 #include <math.h>
 
 #include "serve.h"
@@ -32,10 +33,11 @@ namespace spa {
 namespace {
 
 constexpr int kCtas = 148;             // one per SM
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kTile = 128;             // keys
 constexpr int kMinTiles = 2;           // tiles a run has at least
 constexpr int kRange = 4096;           // blocks whose list is held in shared memory
+constexpr int kShortList = 1024;       // entries up to which a list is read whole
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
@@ -85,9 +87,7 @@ __device__ __forceinline__ int run_total(const TreeArgs &a) {
     if (!a.lens) return a.B * upb * tiles_of(a, 0);
     int s = 0;
     for (int b = lane; b < a.B; b += 32) s += tiles_of(a, b);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s * upb;
+    return __reduce_add_sync(0xffffffffu, s) * upb;
 }
 __device__ __forceinline__ int run_chunk(int total) { return max(kMinTiles, (total + kCtas - 1) / kCtas); }
 __device__ __forceinline__ Where locate(const TreeArgs &a, int pos) {
@@ -142,10 +142,34 @@ __device__ __forceinline__ int lower_bound(const int32_t *list, int cnt, int j) 
     return lo;
 }
 
+// 16 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *x) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+          "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+        : "r"(taddr));
+}
+
+// What a CTA's roles share about the segment (the part of a run inside one unit) and the
+// stretch of its list they are at. It stays in shared memory and is read where it is
+// needed: the softmax holds 128 scores in registers and has none to spare.
+struct Segment {
+    int pos, end;                       // the run's next tile, its end
+    int b, unit, bg, g, P, row0, more;
+    int t_hi, whole, with_tree;         // the unit's tiles end; all of them, the tree here
+    int j_hi;                           // blocks of the text end
+    int s_lo, nu, jobs, ntile, tree_here;   // the stretch: first block, kept blocks, jobs, tiles
+    int clean;                          // tiles of PER whole blocks, ahead of the others
+    int tu, done0, done1, segs;         // key tiles, jobs of each warpgroup, segments so far
+    int had;                            // warpgroups with a job in this segment (bits)
+};
+
 template <int D, int BLK, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                const __grid_constant__ CUtensorMap tv, TreeArgs a) {
+                const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
     using C = Cfg<D, BLK, RT>;
     constexpr int PER = C::PER, NK = C::NK, NV = C::NV;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -156,12 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint64_t bar_q, full_k[NK], empty_k[NK], full_v[NV], empty_v[NV], s_full[2],
         p_ready[2], o_done;
     __shared__ uint32_t tmem_slot;
-    __shared__ int sh_b, sh_unit, sh_t;
-    __shared__ int sh_total;
+    __shared__ Segment sg;
     __shared__ int par[kTile];
     __shared__ uint32_t nmask[kTile][4];          // ancestors and self; all zero: unused
     __shared__ int wcount[kThreads / 32];
-    __shared__ int lo_s[16], hi_s[16];
     __shared__ float st_m[2][kTile], st_l[2][kTile];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -180,59 +202,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tv);
     }
     if (warp == 9) tmem_alloc(&tmem_slot, 512);
-    if (warp == 1) {
-        const int t = run_total(a);
-        if (lane == 0) sh_total = t;
+    if (warp == 0) {
+        const int total = run_total(a), chunk = run_chunk(total);
+        if (lane == 0) {
+            sg.pos = blockIdx.x * chunk;
+            sg.end = min(total, sg.pos + chunk);
+            sg.tu = sg.done0 = sg.done1 = 0;
+            sg.segs = -1;
+        }
     }
+    bool ok = true;                    // cleared by a wait that ran out: no more work, no waits
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    const int chunk = run_chunk(sh_total);
-    int pos = blockIdx.x * chunk;
-    const int end = min(sh_total, pos + chunk);
 
-    bool ok = true;                    // cleared by a wait that ran out: no more work, no waits
-    int tu = 0;                        // key tiles so far (ring position)
-    int jobs_done[2] = {0, 0};         // jobs of each warpgroup so far (barrier phases)
-    int segs = 0;                      // segments so far (phases of bar_q, o_done)
-
-    for (; pos < end; ++segs) {
+    for (;;) {
         // ------------------------------------------------ the segment
         if (warp == 0) {
-            const Where w = locate(a, pos);
+            __syncwarp();
+            const int pos = sg.pos;
+            const bool more = pos < sg.end;
+            Where w = {0, 0, 0};
+            if (more) w = locate(a, pos);
             if (lane == 0) {
-                sh_b = w.b;
-                sh_unit = w.unit;
-                sh_t = w.t;
+                sg.more = more;
+                if (more) {
+                    const int P = text_len(a, w.b), tiles = (P + kTile - 1) / kTile + 1;
+                    sg.b = w.b;
+                    sg.unit = w.unit;
+                    sg.bg = w.unit / a.nrt;
+                    sg.g = sg.bg % a.Hkv;
+                    sg.P = P;
+                    sg.row0 = w.unit % a.nrt * (RT * 128);
+                    sg.t_hi = min(tiles, w.t + sg.end - pos);
+                    sg.with_tree = sg.t_hi == tiles;
+                    sg.whole = w.t == 0 && sg.with_tree;
+                    sg.s_lo = w.t * PER;
+                    sg.j_hi = min((P + BLK - 1) / BLK, sg.t_hi * PER);
+                    sg.pos = pos + sg.t_hi - w.t;
+                    sg.had = 0;
+                    ++sg.segs;
+                    if (a.lens && w.unit % (a.Hkv * a.nrt) == 0 && sg.with_tree) {
+                        const int p = __ldg(a.lens + w.b);
+                        if (p < 0 || p > a.T - a.n) set_error(a.err, SPA_DEVERR_BAD_COUNT);
+                    }
+                }
             }
         }
         __syncthreads();
-        const int b = sh_b, unit = sh_unit, t_lo = sh_t;
-        const int rt = unit % a.nrt, bg = unit / a.nrt, g = bg % a.Hkv;
-        const int P = text_len(a, b);
-        const int text_tiles = (P + kTile - 1) / kTile;
-        const int t_hi = min(text_tiles + 1, t_lo + (end - pos));
-        const bool whole_unit = t_lo == 0 && t_hi == text_tiles + 1;
-        const bool with_tree = t_hi == text_tiles + 1;
-        const int rows = a.G * a.n;
-        const int row0 = rt * RT * 128;              // first row of the unit in its (b, kv-head)
-        const int h_lo = row0 / a.n, h_hi = min(a.G, (min(rows, row0 + RT * 128) - 1) / a.n + 1);
-        const int nb_all = (a.T + BLK - 1) / BLK;
-        if (tid == 0 && a.lens && rt == 0 && g == 0 && with_tree) {
-            const int p = __ldg(a.lens + b);
-            if (p < 0 || p > a.T - a.n) set_error(a.err, SPA_DEVERR_BAD_COUNT);
-        }
+        if (!sg.more) break;
         if (warp == 8 && lane == 0 && ok) {
             mbar_arrive_expect_tx(&bar_q, RT * C::SLOT);
-            const int qrow = (b * a.Hq + g * a.G) * a.n + row0;
+            const int qrow = sg.bg * a.G * a.n + sg.row0;
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int hf = 0; hf < C::HALVES; ++hf)
                     tma_load_2d(smem + r * C::SLOT + hf * C::HALF, &tq, &bar_q, hf * 64, qrow + r * 128);
         }
-        if (tid < a.n) par[tid] = __ldg(a.parents + (size_t)b * a.n + tid);
+        if (tid < a.n) par[tid] = __ldg(a.parents + (size_t)sg.b * a.n + tid);
+        if (a.idx)
+            for (int x = tid; x < kRange / 2; x += kThreads) reinterpret_cast<uint32_t *>(mark)[x] = 0u;
         __syncthreads();
         if (tid < kTile) {
             uint32_t m0 = 0, m1 = 0, m2 = 0, m3 = 0;
@@ -254,65 +284,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             nmask[tid][2] = m2;
             nmask[tid][3] = m3;
         }
-        __syncthreads();
 
-        // this thread's row
-        const int wg = warp >> 2;                                    // 0, 1: softmax
-        const int r = tid & 127;
-        const int row = row0 + (RT == 2 ? wg * 128 : 0) + r;         // in the (b, kv-head)
-        const int node = row % a.n, head = row / a.n;                // head: of the group
-        const bool live = wg < 2 && row < rows &&
-                          (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) != 0u;
-        const bool warp_live = __any_sync(0xffffffffu, live);
         float m_used = -INFINITY, l = 0.f;
-        int first[2] = {1, 1};                                       // MMA: no product in O yet
-        bool any[2] = {false, false};                                // jobs of each warpgroup
-
-        const int j_lo = t_lo * PER, j_hi = min((P + BLK - 1) / BLK, t_hi * PER);
-        for (int s_lo = j_lo;; s_lo += kRange) {
-            const int s_hi = min(j_hi, s_lo + kRange);
-            const bool last = s_hi >= j_hi;
-            const int nr = max(0, s_hi - s_lo);
-            // ---------------------------------------- kept blocks of [s_lo, s_hi)
-            int nu = nr;
-            if (a.idx && nr > 0) {
-                for (int x = tid; x < (nr + 1) / 2; x += kThreads) reinterpret_cast<uint32_t *>(mark)[x] = 0u;
-                for (int hh = h_lo + warp; hh < h_hi; hh += kThreads / 32) {
-                    const size_t u = (size_t)b * a.Hq + g * a.G + hh;
+        int started = 0;                             // MMA: warpgroups with a product in O (bits)
+        for (;;) {
+            // ---------------------------------------- kept blocks of the stretch
+            if (a.idx) {
+                const int s_lo = sg.s_lo, s_hi = min(sg.j_hi, s_lo + kRange), nr = max(0, s_hi - s_lo);
+                const int nb_all = (a.T + BLK - 1) / BLK;
+                // warps and heads in turn; a list's stretch is found by a 32-way search unless
+                // the whole list is short
+                constexpr int kW = kThreads / 32;
+                const int h_lo = sg.row0 / a.n;
+                const int nh = (min(a.G * a.n, sg.row0 + RT * 128) - 1) / a.n + 1 - h_lo;
+                const int share = max(1, kW / nh);                         // warps per head
+                for (int k = warp; k < nh * share; k += kW) {
+                    const int hh = h_lo + k % nh, part = k / nh;
+                    const size_t u = (size_t)sg.bg * a.G + hh;
+                    const int32_t *list = a.idx + u * a.cap;
                     int cnt = __ldg(a.count + u);
                     if (cnt < 0 || cnt > a.cap) {
                         if (lane == 0) set_error(a.err, SPA_DEVERR_BAD_COUNT);
                         cnt = cnt < 0 ? 0 : a.cap;
                     }
-                    const int32_t *list = a.idx + u * a.cap;
-                    const int lo = lower_bound(list, cnt, s_lo), hi = lower_bound(list, cnt, s_hi);
-                    if (lane == 0) {
-                        lo_s[hh] = lo;
-                        hi_s[hh] = hi;
-                        if (cnt > 0 && ((last && with_tree && __ldg(list + cnt - 1) >= nb_all) ||
-                                        (s_lo == 0 && __ldg(list) < 0)))
+                    int lo = 0, hi = cnt;
+                    if (cnt > kShortList) {
+                        lo = lower_bound(list, cnt, s_lo);
+                        hi = lower_bound(list, cnt, s_hi);
+                        if (lane == 0 && part == 0 && sg.with_tree && __ldg(list + cnt - 1) >= nb_all)
                             set_error(a.err, SPA_DEVERR_BAD_INDEX);
                     }
-                }
-                __syncthreads();
-                for (int hh = h_lo; hh < h_hi; ++hh) {
-                    const int32_t *list = a.idx + ((size_t)b * a.Hq + g * a.G + hh) * a.cap;
-                    const int hi = hi_s[hh];
-#pragma unroll 4
-                    for (int p = lo_s[hh] + tid; p < hi; p += kThreads) {
-                        const int j = __ldg(list + p), before = p > 0 ? __ldg(list + p - 1) : -1;
-                        if (j < s_lo || j >= s_hi || before >= j) {
-                            set_error(a.err, SPA_DEVERR_BAD_INDEX);
-                            continue;
+                    constexpr int kAhead = 8;                              // loads in flight per lane
+                    for (int p0 = lo + part * 32; p0 < hi; p0 += share * 32 * kAhead) {
+                        int j[kAhead], before[kAhead];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const int p = p0 + i * share * 32 + lane;
+                            j[i] = p < hi ? __ldg(list + p) : s_hi;
+                            before[i] = p < hi && p > 0 ? __ldg(list + p - 1) : -1;
                         }
-                        const int x = j - s_lo;
-                        atomicOr(reinterpret_cast<unsigned int *>(mark + (x & ~1)),
-                                 (unsigned)(1u << hh) << ((x & 1) * 16));
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            if (p0 + i * share * 32 + lane >= hi) continue;
+                            if (j[i] < 0 || j[i] >= nb_all || before[i] >= j[i]) {
+                                set_error(a.err, SPA_DEVERR_BAD_INDEX);
+                                continue;
+                            }
+                            const int x = j[i] - s_lo;
+                            if (x >= 0 && x < nr)
+                                atomicOr(reinterpret_cast<unsigned int *>(mark + (x & ~1)),
+                                         (unsigned)(1u << hh) << ((x & 1) * 16));
+                        }
                     }
                 }
                 __syncthreads();
                 // close up: each warp a stretch, behind the blocks of the warps before
-                const int steps = (nr + 31) / 32, per = (steps + kThreads / 32 - 1) / (kThreads / 32);
+                const int steps = (nr + 31) / 32, per = (steps + kW - 1) / kW;
                 const int x_lo = min(nr, warp * per * 32), x_hi = min(nr, x_lo + per * 32);
                 int c = 0;
                 for (int x = x_lo; x < x_hi; x += 32)
@@ -320,68 +347,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) wcount[warp] = c;
                 __syncthreads();
                 int at = 0;
-                nu = 0;
-                for (int w = 0; w < kThreads / 32; ++w) {
-                    if (w < warp) at += wcount[w];
-                    nu += wcount[w];
-                }
+                for (int w = 0; w < warp; ++w) at += wcount[w];
                 for (int x = x_lo; x < x_hi; x += 32) {
                     const uint32_t m = x + lane < x_hi ? mark[x + lane] : 0u;
                     const unsigned bal = __ballot_sync(0xffffffffu, m != 0);
                     if (m) ulist[at + __popc(bal & ((1u << lane) - 1u))] = (m << 16) | (uint32_t)(x + lane);
                     at += __popc(bal);
                 }
-                __syncthreads();
             }
-            const int kv_tiles = (nu + PER - 1) / PER;
-            const bool tree_here = last && with_tree;
-            const int ntile = kv_tiles + (tree_here ? 1 : 0);
-            const int jobs = ntile * RT;
-            // block e of tile u: its number in the sequence and the heads that keep it
+            if (a.idx) __syncthreads();
+            if (tid == 0) {
+                int nu;
+                if (a.idx) {
+                    nu = 0;
+                    for (int w = 0; w < kThreads / 32; ++w) nu += wcount[w];
+                    sg.tree_here = sg.with_tree && sg.s_lo + kRange >= sg.j_hi;
+                } else {
+                    nu = max(0, sg.j_hi - sg.s_lo);
+                    sg.tree_here = sg.with_tree;
+                }
+                // Lists ascend: only the last block can be one that the text ends in.
+                const int last_blk = nu > 0 ? (a.idx ? sg.s_lo + (int)(ulist[nu - 1] & 0xffffu) : sg.s_lo + nu - 1) : 0;
+                sg.clean = nu > 0 && nu % PER == 0 && (last_blk + 1) * BLK > sg.P ? nu / PER - 1 : nu / PER;
+                sg.nu = nu;
+                sg.ntile = (nu + PER - 1) / PER + (sg.tree_here ? 1 : 0);
+                sg.jobs = sg.ntile * RT;
+                sg.had |= (sg.jobs > 0 ? 1 : 0) | (sg.jobs > 1 ? 2 : 0);
+            }
+            __syncthreads();
+            const bool last = !a.idx || sg.s_lo + kRange >= sg.j_hi;
+            // block x of the stretch's list: its number in the sequence, the heads that keep it
             auto block_at = [&](int x, uint32_t &heads) -> int {
                 if (!a.idx) {
                     heads = 0xffffu;
-                    return s_lo + x;
+                    return sg.s_lo + x;
                 }
                 const uint32_t w = ulist[x];
                 heads = w >> 16;
-                return s_lo + (int)(w & 0xffffu);
+                return sg.s_lo + (int)(w & 0xffffu);
             };
 
-            if (warp == 8) {
-                // ------------------------------------ producer
+            if (warp == 8 || warp == 10) {
+                // ------------------------------------ producers
                 if (lane == 0 && ok) {
-                    const int kv_row0 = bg * a.T;
+                    const bool is_v = warp == 10;
+                    const int ns = is_v ? NV : NK, kv_row0 = sg.bg * a.T, ntile = sg.ntile, nu = sg.nu;
+                    uint64_t *full = is_v ? full_v : full_k, *empty = is_v ? empty_v : empty_k;
+                    const CUtensorMap *map = is_v ? &tv : &tk;
+                    unsigned char *ring = smem + (is_v ? C::OFF_V : C::OFF_K);
                     for (int u = 0; u < ntile; ++u) {
-                        const int tt = tu + u;
-                        const bool tree = tree_here && u == ntile - 1;
+                        const int tt = sg.tu + u, s = tt % ns;
+                        const bool tree = sg.tree_here && u == ntile - 1;
                         const int nblk = tree ? (a.n + BLK - 1) / BLK : min(PER, nu - u * PER);
+                        int rw[PER];                     // read together, ahead of the copies
 #pragma unroll
-                        for (int kv = 0; kv < 2; ++kv) {
-                            const int ns = kv ? NV : NK, s = tt % ns;
-                            uint64_t *full = kv ? &full_v[s] : &full_k[s];
-                            if (!mbar_wait(kv ? &empty_v[s] : &empty_k[s], ((tt / ns) & 1) ^ 1, a.err)) {
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(full, (uint32_t)(nblk * BLK * D * 2));
-                            unsigned char *dst = smem + (kv ? C::OFF_V : C::OFF_K) + s * C::SLOT;
-                            for (int e = 0; e < nblk; ++e) {
-                                uint32_t hm;
-                                const int rw = tree ? P + e * BLK : block_at(u * PER + e, hm) * BLK;
+                        for (int e = 0; e < PER; ++e) {
+                            uint32_t hm;
+                            rw[e] = kv_row0 + (tree ? sg.P + e * BLK : block_at(min(u * PER + e, nu - 1), hm) * BLK);
+                        }
+                        if (!mbar_wait(&empty[s], ((tt / ns) & 1) ^ 1, a.err)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(nblk * BLK * D * 2));
+                        unsigned char *dst = ring + s * C::SLOT;
+#pragma unroll
+                        for (int e = 0; e < PER; ++e)
+                            if (e < nblk) {
 #pragma unroll
                                 for (int hf = 0; hf < C::HALVES; ++hf)
-                                    tma_load_2d(dst + hf * C::HALF + e * BLK * 128, kv ? &tv : &tk, full,
-                                                hf * 64, kv_row0 + rw);
+                                    tma_load_2d(dst + hf * C::HALF + e * BLK * 128, map, &full[s], hf * 64, rw[e]);
                             }
-                        }
-                        if (!ok) break;
                     }
                 }
             } else if (warp == 9) {
                 // ------------------------------------ products
                 if (lane == 0 && ok) {
-                    if (s_lo == j_lo) ok = mbar_wait(&bar_q, segs & 1, a.err);
+                    const uint32_t tmem = tmem_slot;
+                    const int jobs = sg.jobs, tu = sg.tu, done0 = sg.done0, done1 = sg.done1;
+                    ok = mbar_wait(&bar_q, sg.segs & 1, a.err);
                     auto issue_s = [&](int m) -> bool {
                         const int u = tu + m / RT, w = m & 1, s = u % NK;
                         if (!mbar_wait(&full_k[s], (u / NK) & 1, a.err)) return false;
@@ -401,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int m = 0; m < 2 && m < jobs && ok; ++m) ok = issue_s(m);
                     for (int m = 0; m < jobs && ok; ++m) {
                         const int u = tu + m / RT, w = m & 1, s = u % NV;
-                        ok = mbar_wait(&p_ready[w], (jobs_done[w] + m / 2) & 1, a.err) &&
+                        ok = mbar_wait(&p_ready[w], ((w ? done1 : done0) + m / 2) & 1, a.err) &&
                              mbar_wait(&full_v[s], (u / NV) & 1, a.err);
                         if (!ok) break;
                         tc_fence_after();
@@ -410,66 +454,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int kk = 0; kk < kTile / 16; ++kk)
                             tc_mma_ts(tmem + w * 256 + 128, tmem + w * 256 + kk * 8,
                                       sw128_desc(vb + kk * 2048, C::HALF, 1024), C::IDESC_O,
-                                      (first[w] && kk == 0) ? 0u : 1u);
-                        first[w] = 0;
+                                      (kk > 0 || ((started >> w) & 1)) ? 1u : 0u);
+                        started |= 1 << w;
                         if (RT == 1 || w == 1) tc_commit(&empty_v[s]);
                         if (m + 2 < jobs) ok = issue_s(m + 2);
                     }
                     if (last && ok) tc_commit(&o_done);
                 }
-            } else {
+            } else if (warp < 8) {
                 // ------------------------------------ softmax
-                const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-                const uint32_t t_s = tmem + wg * 256 + lane_off, t_o = t_s + 128;
+                const int wg = warp >> 2, r = tid & 127;
+                const int row = sg.row0 + (RT == 2 ? wg * 128 : 0) + r, node = row % a.n, head = row / a.n & 15;
+                const bool live = row < a.G * a.n &&
+                                  (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) != 0u;
+                const bool warp_live = __any_sync(0xffffffffu, live);
+                const uint32_t t_s = tmem_slot + wg * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
+                const int jobs = sg.jobs, clean = sg.clean, kv_tiles = (sg.nu + PER - 1) / PER;
                 for (int m = wg; m < jobs && ok; m += 2) {
                     const int u = m / RT;
+                    // in a clean tile this row's head keeps a block whole or not at all (bit e)
+                    const bool tree = u >= kv_tiles, dirty = u >= clean;
+                    uint32_t kept = (1u << PER) - 1u;
+                    if (!dirty && a.idx) {
+                        uint32_t w[PER];
+                        if constexpr (PER >= 4) {
+#pragma unroll
+                            for (int e = 0; e < PER; e += 4)
+                                *reinterpret_cast<uint4 *>(w + e) = *reinterpret_cast<const uint4 *>(ulist + u * PER + e);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < PER; ++e) w[e] = ulist[u * PER + e];
+                        }
+                        kept = 0;
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) kept |= ((w[e] >> (16 + head)) & 1u) << e;
+                        if (!live) kept = (1u << PER) - 1u;         // an unused row: anything
+                    }
                     // (votes: a warp gives up as one)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[wg], (jobs_done[wg] + m / 2) & 1, a.err));
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&s_full[wg], ((wg ? sg.done1 : sg.done0) + m / 2) & 1, a.err));
                     if (!ok) break;
                     tc_fence_after();
-                    const bool tree = tree_here && u == ntile - 1;
                     // rows of V that no key of this sequence fills (behind the text, blocks
                     // that are not there, unused nodes) are made zero: their weight is
                     // zero, but 0 x NaN is not
-                    bool dirty = tree;
-                    uint32_t see[4];                 // keys of the tile that this row attends to
-                    if (tree) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) see[c] = live ? nmask[node][c] : 0u;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) see[c] = 0u;
-#pragma unroll
-                        for (int e = 0; e < PER; ++e) {
-                            if (u * PER + e >= nu) {
-                                dirty = true;
-                                continue;
-                            }
-                            uint32_t hm;
-                            const int lim = P - block_at(u * PER + e, hm) * BLK;
-                            dirty = dirty || lim < BLK;
-                            if (!live || !((hm >> head) & 1u)) continue;
-                            if constexpr (BLK == 16) {
-                                see[e / 2] |= (lim >= 16 ? 0xffffu : (1u << max(lim, 0)) - 1u) << (e % 2 * 16);
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < BLK / 32; ++c) {
-                                    const int k = lim - c * 32;
-                                    see[e * (BLK / 32) + c] = k >= 32 ? 0xffffffffu : (1u << max(k, 0)) - 1u;
-                                }
-                            }
-                        }
-                    }
                     if (dirty) {
                         bool fill;
                         if (tree) {
                             fill = (nmask[r][0] | nmask[r][1] | nmask[r][2] | nmask[r][3]) == 0u;
                         } else {
-                            const int x = u * PER + r / BLK;
+                            const int k = u * PER + r / BLK;
                             uint32_t hm;
-                            fill = x >= nu || block_at(x, hm) * BLK + r % BLK >= P;
+                            fill = k >= sg.nu || block_at(k, hm) * BLK + r % BLK >= sg.P;
                         }
-                        const int tt = tu + u, s = tt % NV;
+                        const int tt = sg.tu + u, s = tt % NV;
                         ok = __all_sync(0xffffffffu, mbar_wait(&full_v[s], (tt / NV) & 1, a.err));
                         if (!ok) break;
                         if (fill) {
@@ -487,20 +525,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < kTile / 32; ++c) tmem_ld32f(t_s + c * 32, x + c * 32);
                         tc_wait_ld();
-                        if ((see[0] & see[1] & see[2] & see[3]) != 0xffffffffu) {
+                        if (dirty) {                     // single keys: by a mask of 128 bits
+                            uint32_t see[4] = {0u, 0u, 0u, 0u};
+                            if (tree) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) see[c] = nmask[node][c];
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < PER; ++e) {
+                                    if (u * PER + e >= sg.nu) continue;
+                                    uint32_t hm;
+                                    const int lim = sg.P - block_at(u * PER + e, hm) * BLK;
+                                    if (!((hm >> head) & 1u)) continue;
+                                    if constexpr (BLK == 16) {
+                                        see[e / 2] |= (lim >= 16 ? 0xffffu : (1u << max(lim, 0)) - 1u) << (e % 2 * 16);
+                                    } else {
+#pragma unroll
+                                        for (int c = 0; c < BLK / 32; ++c) {
+                                            const int k = lim - c * 32;
+                                            see[e * (BLK / 32) + c] = k >= 32 ? 0xffffffffu : (1u << max(k, 0)) - 1u;
+                                        }
+                                    }
+                                }
+                            }
 #pragma unroll
                             for (int c = 0; c < kTile; ++c)
                                 x[c] = (see[c >> 5] >> (c & 31)) & 1u ? x[c] : -INFINITY;
                         }
-                        float mp[8];
+                        // maxima block by block, then of the kept ones
+                        float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mp[e] = fmaxf(x[e], x[e + 8]);
+                        for (int e = 0; e < PER; ++e) {
+                            constexpr int CH = BLK >= 64 ? 8 : BLK / 8;      // independent chains
+                            float mp[CH];
 #pragma unroll
-                        for (int c = 16; c < kTile; c += 16)
+                            for (int k = 0; k < CH; ++k) mp[k] = fmaxf(x[e * BLK + k], x[e * BLK + CH + k]);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) mp[e] = fmax3(mp[e], x[c + e], x[c + 8 + e]);
-                        const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]),
-                                               fmaxf(mp[6], mp[7])) * a.scale_log2;
+                            for (int c = 2 * CH; c < BLK; c += 2 * CH)
+#pragma unroll
+                                for (int k = 0; k < CH; ++k)
+                                    mp[k] = fmax3(mp[k], x[e * BLK + c + k], x[e * BLK + c + CH + k]);
+#pragma unroll
+                            for (int k = 1; k < CH; ++k) mp[0] = fmaxf(mp[0], mp[k]);
+                            mx = fmaxf(mx, (kept >> e) & 1u ? mp[0] : -INFINITY);
+                        }
+                        mx *= a.scale_log2;
                         float alpha = 1.f;
                         bool rescale = false;
                         if (mx > m_used + kRescaleThreshold) {
@@ -508,30 +577,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rescale = l > 0.f;
                             m_used = mx;
                         }
-                        const float base = m_used == -INFINITY ? 0.f : m_used;
                         // this warpgroup's previous P V completed before S(m) did: O is stable
                         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o0[32];
-                                tmem_ld32(t_o + c * 32, o0);
+                            for (int c = 0; c < D / 16; ++c) {
+                                float o0[16];
+                                tmem_ld16f(t_o + c * 16, o0);
                                 tc_wait_ld();
+                                uint32_t o1[16];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o0[e] = __float_as_uint(__uint_as_float(o0[e]) * alpha);
-                                tmem_st32(t_o + c * 32, o0);
+                                for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(o0[e] * alpha);
+                                tmem_st16(t_o + c * 16, o1);
                             }
                         }
+                        const float base = m_used == -INFINITY ? 0.f : m_used;
                         uint64_t sp[4] = {0ull, 0ull, 0ull, 0ull};
                         const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
-                        const uint64_t nbase2 = f32x2(-base, -base);
 #pragma unroll
                         for (int c = 0; c < kTile / 32; ++c) {
                             uint32_t w[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
+                                // a block that is not kept: exponents of -inf
+                                const bool k = (kept >> ((c * 32 + 2 * e) / BLK)) & 1u;
+                                const float nb = k ? -base : -INFINITY;
                                 float y0, y1;
                                 f32x2_split(fma_f32x2(f32x2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]),
-                                                      scale2, nbase2), y0, y1);
+                                                      scale2, f32x2(nb, nb)), y0, y1);
                                 const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
                                 sp[e & 3] = add_f32x2(sp[e & 3], f32x2(p0, p1));
                                 w[e] = pack_bf16x2(p0, p1);     // P to bf16 for the tensor cores
@@ -547,21 +619,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&p_ready[wg]);
                 }
             }
-            any[0] = any[0] || jobs > 0;
-            any[1] = any[1] || jobs > 1;
-            tu += ntile;
-            jobs_done[0] += (jobs + 1) / 2;
-            jobs_done[1] += jobs / 2;
             __syncthreads();
+            if (tid == 0) {
+                sg.tu += sg.ntile;
+                sg.done0 += (sg.jobs + 1) / 2;
+                sg.done1 += sg.jobs / 2;
+            }
             if (last) break;
+            if (tid == 0) sg.s_lo += kRange;
+            for (int x = tid; x < kRange / 2; x += kThreads) reinterpret_cast<uint32_t *>(mark)[x] = 0u;
+            __syncthreads();
         }
 
         // ------------------------------------------------ the segment's state
-        if (wg < 2) {
+        if (warp < 8) {
+            const int wg = warp >> 2, r = tid & 127;
+            const int row = sg.row0 + (RT == 2 ? wg * 128 : 0) + r;
+            {                                            // an unused row: no key
+                const int node = row % a.n;
+                if (row >= a.G * a.n || (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) == 0u) {
+                    m_used = -INFINITY;
+                    l = 0.f;
+                }
+            }
             st_m[wg][r] = m_used;
             st_l[wg][r] = l;
             named_bar_sync(1, 256);
-            if (ok) ok = mbar_wait(&o_done, segs & 1, a.err);
+            if (ok) ok = mbar_wait(&o_done, sg.segs & 1, a.err);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             // RT = 1: both warpgroups hold a state of every row; each joins half of the
             // columns. RT = 2: the row's only state.
@@ -573,126 +658,129 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f1 = fast_exp2(st_m[1][r] - mb);
                 l_all = st_l[0][r] * f0 + st_l[1][r] * f1;
             }
-            const bool use0 = RT == 2 ? any[wg] && l > 0.f : any[0] && st_l[0][r] > 0.f;
-            const bool use1 = RT == 1 && any[1] && st_l[1][r] > 0.f;
+            const bool use0 = ok && (RT == 2 ? ((sg.had >> wg) & 1) && l > 0.f : (sg.had & 1) && st_l[0][r] > 0.f);
+            const bool use1 = ok && RT == 1 && (sg.had & 2) && st_l[1][r] > 0.f;
             constexpr int COLS = RT == 1 ? D / 2 : D;
             const int c_lo = RT == 1 ? wg * COLS : 0;
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t t_o0 = tmem + (RT == 2 ? wg * 256 : 0) + 128 + lane_off;
-            const uint32_t t_o1 = tmem + 256 + 128 + lane_off;
+            const uint32_t t_o0 = tmem_slot + (RT == 2 ? wg * 256 : 0) + 128 + lane_off;
+            const uint32_t t_o1 = tmem_slot + 256 + 128 + lane_off;
             const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
-            const bool store = row < rows;
-            const size_t orow = ((size_t)b * a.Hq + g * a.G) * a.n + row;
-            const size_t slot = (size_t)blockIdx.x + unit;       // of this run's state of this unit
-            const int srow = row - row0;
+            const bool store = row < a.G * a.n, whole = sg.whole;
+            const size_t orow = (size_t)sg.bg * a.G * a.n + row;
+            const size_t slot = (size_t)blockIdx.x + sg.unit;    // of this run's state of this unit
+            const int srow = row - sg.row0;
+            if (__any_sync(0xffffffffu, store)) {
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 32) {
-                float o[32];
-                uint32_t v[32];
-                tmem_ld32(t_o0 + c_lo + c, v);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = ok && use0 ? __uint_as_float(v[e]) * f0 : 0.f;
-                if (RT == 1) {
-                    tmem_ld32(t_o1 + c_lo + c, v);
+                for (int c = 0; c < COLS; c += 32) {
+                    float o[32], v[32];
+                    tmem_ld32f(t_o0 + c_lo + c, o);
+                    if (RT == 1) tmem_ld32f(t_o1 + c_lo + c, v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] += ok && use1 ? __uint_as_float(v[e]) * f1 : 0.f;
-                }
-                if (!store) continue;
-                if (whole_unit) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c_lo + c);
+                    for (int e = 0; e < 32; ++e) {
+                        o[e] = use0 ? o[e] * f0 : 0.f;
+                        if (RT == 1) o[e] += use1 ? v[e] * f1 : 0.f;
+                    }
+                    if (!store) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c_lo + c);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        dst[e / 8] = make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
-                                                pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
-                                                pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (slot * RT * 128 + srow) * D + c_lo + c);
+                        for (int e = 0; e < 32; e += 8)
+                            dst[e / 8] = make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
+                                                    pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                                    pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                                    pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                    } else {                              // [D][rows]: a warp's rows side by side
+                        float *dst = a.ws_o + (slot * D + c_lo + c) * (RT * 128) + srow;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; ++e) dst[e * (RT * 128)] = o[e];
+                    }
                 }
             }
             if (store && (RT == 2 || wg == 0)) {
-                if (whole_unit) {
+                if (whole) {
                     if (a.lse) a.lse[orow] = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
                 } else {
-                    float *ml = a.ws_ml + (slot * RT * 128 + srow) * 2;
-                    ml[0] = m_all;
-                    ml[1] = l_all;
+                    reinterpret_cast<float2 *>(a.ws_ml)[slot * (RT * 128) + srow] = make_float2(m_all, l_all);
                 }
             }
             tc_fence_before();
         }
         __syncthreads();
         tc_fence_after();
-        pos += t_hi - t_lo;
     }
     // copies still in flight on a failure path land before the CTA leaves
-    if (warp == 8 && lane == 0) {
-        if (segs > 0) mbar_drain(&bar_q, (segs - 1) & 1);
+    if ((warp == 8 || warp == 10) && lane == 0) {
+        if (warp == 8 && sg.segs >= 0) mbar_drain(&bar_q, sg.segs & 1);
         if (!ok) {
-            drain_ring<NK>(full_k, tu);
-            drain_ring<NV>(full_v, tu);
+            if (warp == 8) drain_ring<NK>(full_k, sg.tu);
+            else drain_ring<NV>(full_v, sg.tu);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem_slot, 512);
     }
 }
 
-// Joins the states of the units that lie in several runs: one warp per row.
+// Joins the states of the units that lie in several runs. A CTA has 32 rows of a unit, one
+// per lane, and 32 features, four per warp.
+constexpr int kJoinWarps = 8, kJoinCols = 4;
 template <int D, int RT>
-__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long orow = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (orow >= (long long)a.B * a.Hq * a.n) return;
-    const int rows = a.G * a.n, bg = (int)(orow / rows), row = (int)(orow - (long long)bg * rows);
-    const int b = bg / a.Hkv, unit = bg * a.nrt + row / (RT * 128);
-    const int chunk = run_chunk(run_total(a));
-    int before = 0;
-    const int tb = tiles_of(a, b);
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+    const int lane = threadIdx.x & 31, c_lo = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinCols;
+    const int unit = blockIdx.x / (RT * 4), srow = blockIdx.x % (RT * 4) * 32 + lane;
+    const int bg = unit / a.nrt, b = bg / a.Hkv, row = unit % a.nrt * (RT * 128) + srow;
+    const int chunk = run_chunk(run_total(a)), tb = tiles_of(a, b);
+    int before = b * tb;
     if (a.lens) {
+        before = 0;
         for (int x = lane; x < b; x += 32) before += tiles_of(a, x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    } else {
-        before = b * tb;
+        before = __reduce_add_sync(0xffffffffu, before);
     }
+    if (row >= a.G * a.n) return;
     const int p0 = before * a.Hkv * a.nrt + (unit - b * a.Hkv * a.nrt) * tb;
-    const int c0 = p0 / chunk, c1 = (p0 + tb - 1) / chunk;
-    if (c0 == c1) return;                       // written by its run
-    const size_t srow = row % (RT * 128);
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml);
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, ml[((size_t)c + unit) * RT * 128 + srow].x);
+    const int c0 = p0 / chunk, ns = (p0 + tb - 1) / chunk - c0 + 1;
+    if (ns == 1) return;                        // written by its run
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + ((size_t)c0 + unit) * (RT * 128) + srow;
+    const float *src = a.ws_o + (((size_t)c0 + unit) * D + c_lo) * (RT * 128) + srow;
+    // online over the runs, four at a time
+    float M = -INFINITY, L = 0.f, o[kJoinCols] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < ns; s0 += 4) {
+        float2 st[4];
+        float v[4][kJoinCols];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mb = M == -INFINITY ? 0.f : M;
-    constexpr int V = D / 32;
-    float L = 0.f, o[V];
+        for (int k = 0; k < 4; ++k) {
+            const bool in = s0 + k < ns;
+            const size_t at = in ? s0 + k : 0;
+            st[k] = ml[at * (RT * 128)];
+            if (!in) st[k].x = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const size_t at = ((size_t)c + unit) * RT * 128 + srow;
-        const float2 s = ml[at];
-        const float f = fast_exp2(s.x - mb);
-        L += s.y * f;
-        const float *src = a.ws_o + at * D + lane * V;
+            for (int e = 0; e < kJoinCols; ++e) v[k][e] = src[(at * D + e) * (RT * 128)];
+        }
+        const float mn = fmaxf(fmaxf(M, fmaxf(st[0].x, st[1].x)), fmaxf(st[2].x, st[3].x));
+        const float mb = mn == -INFINITY ? 0.f : mn, f = fast_exp2(M - mb);
+        L *= f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] += src[e] * f;
+        for (int e = 0; e < kJoinCols; ++e) o[e] *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float g = fast_exp2(st[k].x - mb);
+            L += st[k].y * g;
+#pragma unroll
+            for (int e = 0; e < kJoinCols; ++e) o[e] += v[k][e] * g;
+        }
+        M = mn;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + orow * D + lane * V);
-#pragma unroll
-    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    const size_t orow = (size_t)bg * a.G * a.n + row;
+    *reinterpret_cast<uint2 *>(a.out + orow * D + c_lo) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (a.lse && c_lo == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 bool make_map(CUtensorMap *map, const void *base, uint64_t rows, int d, int box_rows) {
@@ -725,8 +813,8 @@ cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)c.B * c.Hq * c.n + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(c.B * c.Hkv * a.nrt * RT * 4), D / (kJoinWarps * kJoinCols));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -738,7 +826,8 @@ cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
 
 template <int D, int RT>
 cudaError_t launch_d(const TreeCall &c, const TreeArgs &a, cudaStream_t s) {
-    switch (c.block) {
+    // without lists the keys are read 128 at a time, whatever the block
+    switch (c.idx ? c.block : kTile) {
         case 16: return launch_cfg<D, 16, RT>(c, a, s);
         case 32: return launch_cfg<D, 32, RT>(c, a, s);
         case 64: return launch_cfg<D, 64, RT>(c, a, s);
