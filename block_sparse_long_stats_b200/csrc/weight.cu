@@ -3,7 +3,7 @@
 //   w_t = sum_c exp(s q_c.k_t - lse_c) over the queries c of the key's kv-head that see t
 //
 // The score tile is taken transposed, S^T = K Q^T: 128 keys are the rows (TMEM lanes)
-// and up to 128 queries the columns, so a thread owns one key and its sum runs over its
+// and up to 256 queries the columns, so a thread owns one key and its sum runs over its
 // own registers, with no reduction between threads. The log-sum-exp is an input, so
 // one pass over K is enough. Decode (a few queries) is bound by reading K once (256
 // bytes per key at d = 128); with some hundred queries and more the exponentials bound it
@@ -17,9 +17,12 @@
 // tile of a run do), and a second kernel adds them in order: no atomics, so a call repeats
 // bit for bit.
 //
-// Warp roles: warps 0-15: four warpgroups that take the pairs in turn, each with a score
-// tile of its own in tensor memory; warp 16: TMA producer; warp 17: TMEM allocator and
-// tcgen05.mma issuer.
+// Warp roles: warps 0-15: four warpgroups; up to 128 columns they take the pairs in turn,
+// each with a score tile of its own in tensor memory, with more (STREAM) two of them
+// share a tile of 256 columns, 128 each (the N = 256 product runs at the full rate, 128
+// cycles a step, where N = 128 takes 102-118, and half as many pairs pass the issuing
+// thread); warps 16, 18: TMA producers (query tiles, and a half of every key tile each);
+// warp 17: TMEM allocator and tcgen05.mma issuer.
 #include <math.h>
 
 #include "serve.h"
@@ -30,13 +33,14 @@ namespace {
 constexpr int kCtas = 148;             // one per SM
 constexpr int kGroups = 4;             // consumer warpgroups
 constexpr int kConsumers = kGroups * 128;
-constexpr int kThreads = kConsumers + 64;
+constexpr int kThreads = kConsumers + 96;
 constexpr int kTile = 128;             // keys
 constexpr int kMarkChunk = 2048;       // blocks per CTA of the mark kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightArgs {
     const int32_t *lens;
+    const __nv_bfloat16 *q;
     const float *lse, *prev;
     const uint16_t *marks;             // [B, Hkv, nq, nbp] head masks of the kept blocks, or null
     float *out, *parts;                // parts [2 kCtas][kTile]
@@ -55,7 +59,10 @@ struct Cfg {
     static constexpr int Q_SLOT = HALVES * Q_HALF;
     // streams of query tiles want a deep query ring, a stream of key tiles a deep key ring
     static constexpr int NK = STREAM ? 2 : (D == 64 ? 8 : 4);
-    static constexpr int NQ = STREAM ? 4 : 2;
+    static constexpr int NQ = 2;
+    static constexpr int SHARE = STREAM ? 2 : 1;           // warpgroups per score tile
+    static constexpr int BUFS = kGroups / SHARE;           // score tiles in tensor memory
+    static constexpr int COLS = NC / SHARE;                // columns of a warpgroup
     static constexpr int OFF_Q = NK * K_SLOT;
     static constexpr int SMEM = OFF_Q + NQ * Q_SLOT + 1024;
     static constexpr uint32_t IDESC = idesc_bf16(128, NC, false);
@@ -169,6 +176,9 @@ __device__ __forceinline__ Pair locate(const WeightArgs &a, long long pos) {
     }
 }
 
+// -lse in log2 units, so that exp2(s log2e q.k + it) is the weight: 0 for a row of -inf.
+__device__ __forceinline__ float minus_log2(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
 // Sets bits [lo, hi) of a 128-bit mask.
 __device__ __forceinline__ void set_range(uint32_t (&m)[4], int lo, int hi) {
 #pragma unroll
@@ -180,27 +190,37 @@ __device__ __forceinline__ void set_range(uint32_t (&m)[4], int lo, int hi) {
     }
 }
 
+// 16 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *x) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+          "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+        : "r"(taddr));
+}
+
 template <int D, int NC, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                  WeightArgs a) {
+                  const __grid_constant__ WeightArgs a) {
     using C = Cfg<D, NC, STREAM>;
-    constexpr int NK = C::NK, NQ = C::NQ;
+    constexpr int NK = C::NK, NQ = C::NQ, BUFS = C::BUFS, COLS = C::COLS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full_k[NK], empty_k[NK], full_q[NQ], empty_q[NQ], s_full[kGroups], s_empty[kGroups];
+    __shared__ uint64_t full_k[NK], empty_k[NK], full_q[NQ], empty_q[NQ], s_full[BUFS], s_empty[BUFS];
     __shared__ uint32_t tmem_slot;
     __shared__ Pair sh_pair;
     __shared__ long long sh_total;
-    __shared__ __align__(16) float nl_s[kGroups][NC];   // -lse of the columns, log2 units
+    __shared__ __align__(16) float nl_s[kGroups][COLS]; // -lse of the columns, log2 units
     __shared__ float red[2][kGroups][kTile];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 1); mbar_init(&empty_k[s], 1); }
+        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 2); mbar_init(&empty_k[s], 1); }
         for (int s = 0; s < NQ; ++s) { mbar_init(&full_q[s], 1); mbar_init(&empty_q[s], 1); }
-        for (int w = 0; w < kGroups; ++w) { mbar_init(&s_full[w], 1); mbar_init(&s_empty[w], 128); }
+        for (int w = 0; w < BUFS; ++w) { mbar_init(&s_full[w], 1); mbar_init(&s_empty[w], 128 * C::SHARE); }
         fence_mbar_init();
     }
     // query rows that no copy fills stay zero (finite scores; their columns count nothing)
@@ -215,10 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         const long long t = run_total(a), pos = (long long)blockIdx.x * run_chunk(t);
         if (lane == 0) sh_total = t;
-        if (pos < t) {
-            const Pair p = locate(a, pos);
-            if (lane == 0) sh_pair = p;
-        }
+        Pair p = {0, 0, 0, 0, 1, 0};             // a run without a pair: not used
+        if (pos < t) p = locate(a, pos);
+        if (lane == 0) sh_pair = p;
     }
     tc_fence_before();
     __syncthreads();
@@ -229,15 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long jobs = max(0ll, min(sh_total, pos0 + chunk) - pos0);
     const bool gq1 = a.nq == 1;
 
-    if (warp == 16) {
-        // ---------------------------------------------------- producer
+    if (warp == 16 || warp == 18) {
+        // ---------------------------------------------------- producers
+        // warp 16 copies the query tiles; of a key tile each copies a part: a 64-column half
+        // (d = 128), or every other block
         bool ok = true;
+        const int part = warp == 18;
         int nk = 0, nqs = 0;
         Pair p = sh_pair;
         bool new_k = true, new_q = true;
+        const int per = kTile / a.block;
         int kept = 0, kept_at = -1;      // lane i: kept blocks of key tile kept_at + i
         for (long long m = 0; m < jobs && ok; ++m) {
-            if (new_q && lane == 0) {
+            if (new_q && lane == 0 && part == 0) {
                 const int s = nqs % NQ;
                 ok = mbar_wait(&empty_q[s], ((nqs / NQ) & 1) ^ 1, a.err);
                 if (ok) {
@@ -255,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (new_q) ++nqs;
             if (new_k) {
-                const int per = kTile / a.block;
                 int want = (1 << per) - 1;
                 if (a.marks && gq1) {    // one list per head: blocks that no head keeps are not read
                     if (kept_at < 0 || p.kt >= kept_at + 32 || p.kt < kept_at || p.kt == 0) {
@@ -270,18 +292,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     want = __shfl_sync(0xffffffffu, kept, p.kt - kept_at);
                 }
+                if (D == 64) want &= part ? 0xaa : 0x55;
                 if (lane == 0 && ok) {
                     const int s = nk % NK;
                     ok = mbar_wait(&empty_k[s], ((nk / NK) & 1) ^ 1, a.err);
                     if (ok) {
-                        mbar_arrive_expect_tx(&full_k[s], (uint32_t)(__popc(want) * a.block * D * 2));
-                        for (int e = 0; e < per; ++e)
-                            if ((want >> e) & 1) {
+                        mbar_arrive_expect_tx(&full_k[s], (uint32_t)(__popc(want) * a.block * 128));
+                        const int hf = D == 128 ? part : 0, row = p.bg * a.T + p.kt * kTile;
+                        unsigned char *dst = smem + s * C::K_SLOT + hf * C::K_HALF;
 #pragma unroll
-                                for (int hf = 0; hf < C::HALVES; ++hf)
-                                    tma_load_2d(smem + s * C::K_SLOT + hf * C::K_HALF + e * a.block * 128, &tk,
-                                                &full_k[s], hf * 64, p.bg * a.T + p.kt * kTile + e * a.block);
-                            }
+                        for (int e = 0; e < 8; ++e)
+                            if ((want >> e) & 1)
+                                tma_load_2d(dst + e * a.block * 128, &tk, &full_k[s], hf * 64, row + e * a.block);
                     }
                 }
                 ++nk;
@@ -289,48 +311,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             bool head;
             new_k = p.next(a, head);
-            new_q = STREAM || head;
+            new_q = head || a.nqt > 1;
         }
         if (lane == 0 && !ok) {
             drain_ring<NK>(full_k, nk);
-            drain_ring<NQ>(full_q, nqs);
+            if (part == 0) drain_ring<NQ>(full_q, nqs);
         }
     } else if (warp == 17) {
         // ---------------------------------------------------- products
         if (lane == 0) {
+            // With one query tile per head two key tiles are multiplied together, step by step
+            // in turn: a narrow product's steps wait for one another (some 100 cycles each)
+            constexpr int TWO = STREAM ? 1 : 2;
             bool ok = true, new_k = true, new_q = true;
             int nk = 0, nqs = 0;
             Pair p = sh_pair;
-            for (long long m = 0; m < jobs && ok; ++m) {
-                const int w = (int)(m & (kGroups - 1));
-                if (new_k) { ok = mbar_wait(&full_k[nk % NK], (nk / NK) & 1, a.err); ++nk; }
-                if (new_q && ok) { ok = mbar_wait(&full_q[nqs % NQ], (nqs / NQ) & 1, a.err); }
-                if (new_q) ++nqs;
-                if (ok) ok = mbar_wait(&s_empty[w], (uint32_t)((m / kGroups) & 1) ^ 1u, a.err);
+            for (long long m = 0; m < jobs && ok; m += TWO) {
+                uint32_t kb[TWO], qb[TWO];
+                int k_used[TWO], q_used[TWO], free_q[TWO];
+                const int n = TWO == 1 || m + 1 == jobs ? 1 : 2;
+#pragma unroll
+                for (int i = 0; i < TWO; ++i) {
+                    free_q[i] = 0;
+                    if (i >= n || !ok) continue;
+                    if (new_k) { ok = mbar_wait(&full_k[nk % NK], (nk / NK) & 1, a.err); ++nk; }
+                    if (new_q && ok) ok = mbar_wait(&full_q[nqs % NQ], (nqs / NQ) & 1, a.err);
+                    if (new_q) ++nqs;
+                    if (ok) ok = mbar_wait(&s_empty[(m + i) % BUFS], (uint32_t)(((m + i) / BUFS) & 1) ^ 1u, a.err);
+                    k_used[i] = (nk - 1) % NK;
+                    q_used[i] = (nqs - 1) % NQ;
+                    kb[i] = smem_u32(smem + k_used[i] * C::K_SLOT);
+                    qb[i] = smem_u32(smem + C::OFF_Q + q_used[i] * C::Q_SLOT);
+                    bool head;
+                    new_k = p.next(a, head);
+                    new_q = head || a.nqt > 1;
+                    free_q[i] = new_q;
+                }
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t kb = smem_u32(smem + ((nk - 1) % NK) * C::K_SLOT);
-                const uint32_t qb = smem_u32(smem + C::OFF_Q + ((nqs - 1) % NQ) * C::Q_SLOT);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_ss(tmem + w * 128, sw128_desc(kb + (kk >> 2) * C::K_HALF + (kk & 3) * 32, 16, 1024),
-                              sw128_desc(qb + (kk >> 2) * C::Q_HALF + (kk & 3) * 32, 16, 1024), C::IDESC,
-                              kk > 0 ? 1u : 0u);
-                tc_commit(&s_full[w]);
-                const int k_used = (nk - 1) % NK, q_used = (nqs - 1) % NQ;
-                bool head;
-                new_k = p.next(a, head);
-                new_q = STREAM || head;
-                if (new_k) tc_commit(&empty_k[k_used]);
-                if (new_q) tc_commit(&empty_q[q_used]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ko = (kk >> 2) * C::K_HALF + (kk & 3) * 32, qo = (kk >> 2) * C::Q_HALF + (kk & 3) * 32;
+#pragma unroll
+                    for (int i = 0; i < TWO; ++i)
+                        if (i < n)
+                            tc_mma_ss(tmem + (int)((m + i) % BUFS) * (512 / BUFS), sw128_desc(kb[i] + ko, 16, 1024),
+                                      sw128_desc(qb[i] + qo, 16, 1024), C::IDESC, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < TWO; ++i) {
+                    if (i >= n) continue;
+                    tc_commit(&s_full[(m + i) % BUFS]);
+                    if (!STREAM || new_k) tc_commit(&empty_k[k_used[i]]);
+                    if (free_q[i]) tc_commit(&empty_q[q_used[i]]);
+                }
             }
         }
     } else {
         // ---------------------------------------------------- sums
         const int wg = warp >> 2, r = tid & 127;
+        const int buf = wg / C::SHARE, col0 = wg % C::SHARE * COLS;
         const uint32_t t_s = tmem + wg * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-        const int ch = r / a.pc, ci = r - ch * a.pc;       // column r: head of the group, position
-        const bool col = r < NC && ch < a.G;
+        const int ch = (col0 + r) / a.pc, ci = col0 + r - ch * a.pc;   // this thread's column: head, position
+        const bool col = r < COLS && ch < a.G;
         // keys behind every sequence: no weight
         for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
             const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kTile - 1) / kTile * kTile;
@@ -344,6 +387,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         Pair p = sh_pair;
+        // the log-sum-exp of this thread's column of a pair's query tile; no row there: as if
+        // it saw nothing
+        auto column = [&](const Pair &x) -> float {
+            if (!col || x.qi * a.pc + ci >= a.Lq) return -INFINITY;
+            return __ldg(a.lse + ((size_t)x.bg * a.G + ch) * a.Lq + x.qi * a.pc + ci);
+        };
+        Pair pn = p;                           // this group's next pair
+        float nl_next = 0.f;
+        if (a.nqt > 1 && buf < jobs) {
+            for (int i = 0; i < buf; ++i) {
+                bool head;
+                pn.next(a, head);
+            }
+            nl_next = column(pn);
+        }
         bool ok = true, fresh = true;          // fresh: this group's columns changed
         float sum = 0.f;
         int units = 0;
@@ -351,17 +409,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first_qi = jobs > 0 ? first_tile(a, p.kt, p.off) : 0;
         bool from_start = jobs > 0 && p.qi == first_qi;
         for (long long m = 0; m < jobs; ++m) {
-            const bool mine = (m & (kGroups - 1)) == wg;
+            const bool mine = m % BUFS == buf;
             const int t = p.kt * kTile + r;
             const size_t o = (size_t)p.bg * a.T + t;
             const bool last_pair = p.qi == a.nqt - 1;      // of the key tile
             if (mine) {
-                // loads that need no score: ahead of the wait
-                float nl = -INFINITY;
-                if (fresh && col && p.qi * a.pc + ci < a.Lq) {
-                    const int g = p.bg % a.Hkv;
-                    const float x = __ldg(a.lse + ((size_t)p.b * a.Hq + g * a.G + ch) * a.Lq + p.qi * a.pc + ci);
-                    nl = x == -INFINITY ? -INFINITY : -x * kLog2e;
+                // loads that need no score: ahead of the wait (the columns' lse a job ahead)
+                const float nl = nl_next;
+                if (a.nqt > 1 && m + BUFS < jobs) {
+#pragma unroll
+                    for (int i = 0; i < BUFS; ++i) {
+                        bool head;
+                        pn.next(a, head);
+                    }
+                    nl_next = column(pn);
                 }
                 float before = 0.f;
                 if (!STREAM && a.prev && t < a.T) before = a.prev[o];
@@ -376,9 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int blk = t / a.block, qb0 = p.off / a.block;
                     if (t < a.T) {
                         const uint16_t *mk = a.marks + (size_t)p.bg * a.nq * a.nbp + blk;
-                        if (!STREAM && a.pc == 1) {
-                            see[0] = mk[0];
-                        } else {
+                        {
                             const int q_end = min(a.Lq, (p.qi + 1) * a.pc) + p.off;
                             for (int qb = q0 / a.block; qb * a.block < q_end; ++qb) {
                                 const uint32_t hm = mk[(size_t)(qb - qb0) * a.nbp];
@@ -386,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const int hi = min((qb + 1) * a.block, q_end) - q0;
                                 if (lo < hi)
                                     for (int h = 0; h < a.G; ++h)
-                                        if ((hm >> h) & 1u) set_range(see, h * a.pc + lo, h * a.pc + hi);
+                                        if ((hm >> h) & 1u) set_range(see, h * a.pc + lo - col0, h * a.pc + hi - col0);
                             }
                         }
                     }
@@ -395,41 +454,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) see[c] = 0u;
                     if (lim < a.pc)
-                        for (int h = 0; h < a.G; ++h) set_range(see, h * a.pc + max(lim, 0), (h + 1) * a.pc);
+                        for (int h = 0; h < a.G; ++h) set_range(see, h * a.pc + max(lim, 0) - col0, (h + 1) * a.pc - col0);
                 }
                 if (fresh) {
                     named_bar_sync(2 + wg, 128);           // the group is done with the last columns
-                    if (r < NC) nl_s[wg][r] = nl;
+                    if (r < COLS) nl_s[wg][r] = minus_log2(a.nqt > 1 ? nl : column(p));
                     named_bar_sync(2 + wg, 128);
                 }
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[wg], (uint32_t)((m / kGroups) & 1), a.err));
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (uint32_t)((m / BUFS) & 1), a.err));
                 if (ok) {
                     tc_fence_after();
                     uint64_t acc[2] = {0ull, 0ull};
                     const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
-                    constexpr int STEP = NC < 32 ? 16 : 32;
+                    float x[2][16];
+                    tmem_ld16f(t_s, x[0]);
 #pragma unroll
-                    for (int c0 = 0; c0 < NC; c0 += STEP) {
-                        float x[32];
-                        if constexpr (STEP == 32) {
-                            tmem_ld32f(t_s + c0, x);
-                        } else {
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                                : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
-                                  "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]),
-                                  "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
-                                : "r"(t_s));
-                        }
+                    for (int c0 = 0; c0 < COLS; c0 += 16) {
                         tc_wait_ld();
-                        const uint32_t bits = masked ? see[c0 >> 5] : 0xffffffffu;
+                        const float *y = x[(c0 / 16) & 1];
+                        if (c0 + 16 < COLS) tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
+                        const uint32_t bits = masked ? see[c0 >> 5] >> (c0 & 16) : 0xffffu;
 #pragma unroll
-                        for (int e = 0; e < STEP; e += 4) {
+                        for (int e = 0; e < 16; e += 4) {
                             const float4 n4 = *reinterpret_cast<const float4 *>(&nl_s[wg][c0 + e]);
                             float y0, y1, y2, y3;
-                            f32x2_split(fma_f32x2(f32x2(x[e], x[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
-                            f32x2_split(fma_f32x2(f32x2(x[e + 2], x[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
+                            f32x2_split(fma_f32x2(f32x2(y[e], y[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
+                            f32x2_split(fma_f32x2(f32x2(y[e + 2], y[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
                             if (masked) {          // a key no one keeps may hold anything: select
                                 y0 = (bits >> e) & 1u ? y0 : -INFINITY;
                                 y1 = (bits >> (e + 1)) & 1u ? y1 : -INFINITY;
@@ -444,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
                     sum += s0 + s1;
                     tc_fence_before();
-                    mbar_arrive(&s_empty[wg]);
+                    mbar_arrive(&s_empty[buf]);
                 }
                 fresh = false;
                 if (!STREAM) {                              // the key tile's only pair
@@ -476,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bool head;
             p.next(a, head);
-            fresh = fresh || STREAM || head;
+            fresh = fresh || head || a.nqt > 1;
         }
     }
     tc_fence_before();
@@ -487,10 +537,227 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------- a few queries
+// Up to 16 query rows per kv-head (decode): a step of tcgen05.mma over 128 keys takes over
+// 100 cycles however few its columns, more than the 1000 a tile's bytes leave, so the
+// scores come from mma.sync: a warp takes 16 keys of a tile as the rows and the queries as
+// 8 or 16 columns, the keys' fragments by ldmatrix from the swizzled tile. A quad of lanes
+// holds a key's row and adds its weights. Two groups of eight warps take the tiles in turn.
+// Bound by HBM: each key is read once.
+constexpr int kFewWarps = 16;
+constexpr int kFewThreads = kFewWarps * 32 + 64;
+constexpr int kFewRing = 196608;         // bytes of key tiles in flight
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    weight_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ WeightArgs a) {
+    constexpr int HALVES = D / 64, K_HALF = kTile * 128, K_SLOT = HALVES * K_HALF, NK = kFewRing / K_SLOT;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full_k[NK], empty_k[NK];
+    __shared__ Pair sh_pair;
+    __shared__ long long sh_total;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 2); mbar_init(&empty_k[s], kFewWarps / 2); }
+        fence_mbar_init();
+    }
+    if (warp == kFewWarps && lane == 0) prefetch_tmap(&tk);
+    if (warp == 0) {
+        const long long t = run_total(a), pos = (long long)blockIdx.x * run_chunk(t);
+        if (lane == 0) sh_total = t;
+        Pair p = {0, 0, 0, 0, 1, 0};             // a run without a pair: not used
+        if (pos < t) p = locate(a, pos);
+        if (lane == 0) sh_pair = p;
+    }
+    __syncthreads();
+    if (a.marks) asm volatile("griddepcontrol.wait;" ::: "memory");   // the mark kernel's output
+    const long long chunk = run_chunk(sh_total), pos0 = (long long)blockIdx.x * chunk;
+    const int tiles = (int)max(0ll, min(sh_total, pos0 + chunk) - pos0);
+    Pair p = sh_pair;
+
+    if (warp >= kFewWarps) {
+        // ---------------------------------------------------- producers: a part of each tile each
+        const int part = warp - kFewWarps, per = kTile / a.block;
+        int kept = 0, kept_at = -1, nk = 0;      // lane i: kept blocks of key tile kept_at + i
+        bool ok = true;
+        for (int m = 0; m < tiles && ok; ++m) {
+            int want = (1 << per) - 1;
+            if (a.marks && a.nq == 1) {          // blocks that no head keeps are not read
+                if (kept_at < 0 || p.kt >= kept_at + 32 || p.kt == 0) {
+                    kept_at = p.kt;
+                    kept = 0;
+                    const int kt = p.kt + lane;
+                    if (kt < p.nt)
+                        for (int e = 0; e < per; ++e) {
+                            const int j = kt * per + e;
+                            if (j < a.nbp && a.marks[(size_t)p.bg * a.nbp + j]) kept |= 1 << e;
+                        }
+                }
+                want = __shfl_sync(0xffffffffu, kept, p.kt - kept_at);
+            }
+            if (D == 64) want &= part ? 0xaa : 0x55;
+            if (lane == 0) {
+                const int s = m % NK;
+                ok = mbar_wait(&empty_k[s], ((m / NK) & 1) ^ 1, a.err);
+                if (ok) {
+                    mbar_arrive_expect_tx(&full_k[s], (uint32_t)(__popc(want) * a.block * 128));
+                    const int hf = D == 128 ? part : 0, row = p.bg * a.T + p.kt * kTile;
+                    unsigned char *dst = smem + s * K_SLOT + hf * K_HALF;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((want >> e) & 1)
+                            tma_load_2d(dst + e * a.block * 128, &tk, &full_k[s], hf * 64, row + e * a.block);
+                    ++nk;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            bool head;
+            p.next(a, head);
+        }
+        if (lane == 0) drain_ring<NK>(full_k, nk);
+    } else {
+        // ---------------------------------------------------- weights
+        const int grp = warp >> 3, slab = warp & 7, gq = lane >> 2, tq = lane & 3;
+        // keys behind every sequence: no weight
+        for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
+            const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kTile - 1) / kTile * kTile;
+            if (a.lens && tid == 0 && bg % a.Hkv == 0) {
+                const int n = __ldg(a.lens + b);
+                if (n < a.Lq || n > a.T) set_error(a.err, SPA_DEVERR_BAD_COUNT);
+            }
+            for (int t = t0 + tid; t < a.T; t += kFewWarps * 32) {
+                const size_t o = (size_t)bg * a.T + t;
+                a.out[o] = a.prev ? a.decay * a.prev[o] : 0.f;
+            }
+        }
+        const int rows = a.G * a.Lq;
+        uint32_t qf[NT][D / 16][2];
+        float nl[NT][2];
+        int ci[NT][2], ch[NT][2];                // position and head of the lane's columns
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = t * 8 + 2 * tq + e;
+                ch[t][e] = c / a.Lq;
+                ci[t][e] = c - ch[t][e] * a.Lq;
+            }
+        bool fresh = true, ok = true;
+        for (int m = 0; m < tiles && ok; ++m) {
+            if ((m & 1) == grp) {
+                if (fresh) {                     // a new (b, kv-head): its rows lie together in q and lse
+                    fresh = false;
+                    const size_t row0 = (size_t)p.bg * rows;
+                    const uint32_t *q32 = reinterpret_cast<const uint32_t *>(a.q);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const bool in = t * 8 + gq < rows;
+                        const uint32_t *qr = q32 + (row0 + (in ? t * 8 + gq : 0)) * (D / 2);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            qf[t][ks][0] = in ? __ldg(qr + ks * 8 + tq) : 0u;
+                            qf[t][ks][1] = in ? __ldg(qr + ks * 8 + tq + 4) : 0u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = t * 8 + 2 * tq + e;
+                            nl[t][e] = c < rows ? minus_log2(__ldg(a.lse + row0 + c)) : -INFINITY;
+                        }
+                    }
+                }
+                const int t0 = p.kt * kTile + slab * 16 + gq, t1 = t0 + 8;     // the lane's keys
+                const size_t o = (size_t)p.bg * a.T;
+                float b0 = 0.f, b1 = 0.f;
+                if (a.prev && tq == 0) {
+                    if (t0 < a.T) b0 = a.prev[o + t0];
+                    if (t1 < a.T) b1 = a.prev[o + t1];
+                }
+                // which of its columns see a key: behind it, and kept by the column's head
+                uint32_t see = 0u;                                   // bit 4 t + 2 e + key
+                {
+                    const uint16_t *mk = a.marks ? a.marks + (size_t)p.bg * a.nq * a.nbp : nullptr;
+                    const int blk0 = t0 / a.block, blk1 = t1 / a.block, qb0 = p.off / a.block;
+                    const uint32_t one0 = mk && a.nq == 1 && t0 < a.T ? mk[blk0] : 0xffffu;
+                    const uint32_t one1 = mk && a.nq == 1 && t1 < a.T ? mk[blk1] : 0xffffu;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = p.off + ci[t][e];         // the column's position
+                            uint32_t h0 = one0, h1 = one1;
+                            if (mk && a.nq > 1 && ci[t][e] < a.Lq && ch[t][e] < a.G) {
+                                const size_t l = (size_t)(at / a.block - qb0) * a.nbp;
+                                h0 = t0 < a.T ? mk[l + blk0] : 0u;
+                                h1 = t1 < a.T ? mk[l + blk1] : 0u;
+                            }
+                            if (t0 <= at && ((h0 >> ch[t][e]) & 1u)) see |= 1u << (4 * t + 2 * e);
+                            if (t1 <= at && ((h1 >> ch[t][e]) & 1u)) see |= 2u << (4 * t + 2 * e);
+                        }
+                }
+                const int s = m % NK;
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_k[s], (m / NK) & 1, a.err));
+                if (!ok) break;
+                const uint32_t kt = smem_u32(smem + s * K_SLOT);
+                float c[NT][2][4];               // two chains per column tile
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[t][0][e] = c[t][1][e] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    // 16 keys x 16 features: rows (lane & 7) + 8 (lane >> 3 & 1), 16-byte chunk by lane >> 4
+                    const int row = slab * 16 + (lane & 15), ck = ks * 2 + (lane >> 4);
+                    const uint32_t addr = kt + (ck >> 3) * K_HALF + row * 128 + (((ck & 7) ^ (row & 7)) << 4);
+                    uint32_t k0, k1, k2, k3;
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(k0), "=r"(k1), "=r"(k2), "=r"(k3) : "r"(addr));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        asm volatile(
+                            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                            "{%8,%9}, {%0,%1,%2,%3};"
+                            : "+f"(c[t][ks & 1][0]), "+f"(c[t][ks & 1][1]), "+f"(c[t][ks & 1][2]), "+f"(c[t][ks & 1][3])
+                            : "r"(k0), "r"(k1), "r"(k2), "r"(k3), "r"(qf[t][ks][0]), "r"(qf[t][ks][1]));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty_k[s]);
+                float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = fmaf(c[t][0][e] + c[t][1][e], a.scale_log2, nl[t][e]);
+                        const float y1 = fmaf(c[t][0][2 + e] + c[t][1][2 + e], a.scale_log2, nl[t][e]);
+                        // rows that no copy filled may hold anything: select
+                        w0 += (see >> (4 * t + 2 * e)) & 1u ? fast_exp2(y0) : 0.f;
+                        w1 += (see >> (4 * t + 2 * e)) & 2u ? fast_exp2(y1) : 0.f;
+                    }
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+                if (tq == 0) {
+                    const int len = p.off + a.Lq;
+                    if (t0 >= len) w0 = 0.f;
+                    if (t1 >= len) w1 = 0.f;
+                    if (t0 < a.T) a.out[o + t0] = a.prev ? fmaf(a.decay, b0, w0) : w0;
+                    if (t1 < a.T) a.out[o + t1] = a.prev ? fmaf(a.decay, b1, w1) : w1;
+                }
+            }
+            bool head;
+            p.next(a, head);
+            fresh = fresh || head;
+        }
+    }
+}
+
 // Adds the partial sums of the key tiles that lie in several runs: CTA c looks after the
 // tile that run c begins inside of, if that tile began in run c - 1 or before and no
 // run between begins inside of it too.
-__global__ void __launch_bounds__(kTile) weight_join_kernel(WeightArgs a) {
+__global__ void __launch_bounds__(kTile) weight_join_kernel(const __grid_constant__ WeightArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int r = threadIdx.x;
     const long long total = run_total(a), chunk = run_chunk(total);
@@ -618,18 +885,33 @@ cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
     void *args[] = {&mq, &mk, &a};
     e = launch_after(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kThreads), C::SMEM, args,
                      a.marks != nullptr, s);
-    if (e != cudaSuccess || !STREAM) return e;
+    if (e != cudaSuccess || a.nqt == 1) return e;      // one pair per key tile: no partial sums
     void *jargs[] = {&a};
     return launch_after(reinterpret_cast<const void *>(weight_join_kernel), dim3(kCtas), dim3(kTile), 0, jargs,
                         true, s);
 }
 
+template <int D, int NT>
+cudaError_t launch_few(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
+    CUtensorMap mq, mk;
+    if (!make_maps(&mq, &mk, c, a.pc)) return cudaErrorNotSupported;
+    constexpr int smem = kFewRing + 1024;
+    const void *kern = reinterpret_cast<const void *>(weight_few_kernel<D, NT>);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long most = (long long)c.B * c.Hkv * ((c.T + kTile - 1) / kTile);
+    void *args[] = {&mk, &a};
+    return launch_after(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kFewThreads), smem, args,
+                        a.marks != nullptr, s);
+}
+
 template <int D>
 cudaError_t launch_d(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
-    // query tiles of 128 rows, in a stream; or one tile as narrow as the rows allow
-    if (a.nqt > 1) return launch_cfg<D, 128, true>(c, a, s);
+    // query tiles of up to 256 rows, in a stream; or one tile as narrow as the rows allow
+    if (a.G * a.pc > 128) return launch_cfg<D, 256, true>(c, a, s);
     const int rows = a.G * a.pc;
-    if (rows <= 16) return launch_cfg<D, 16, false>(c, a, s);
+    if (rows <= 8) return launch_few<D, 1>(c, a, s);
+    if (rows <= 16) return launch_few<D, 2>(c, a, s);
     if (rows <= 64) return launch_cfg<D, 64, false>(c, a, s);
     return launch_cfg<D, 128, false>(c, a, s);
 }
@@ -651,11 +933,12 @@ size_t weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block) {
 
 cudaError_t launch_weight(const WeightCall &c, cudaStream_t s) {
     WeightArgs a;
+    a.q = static_cast<const __nv_bfloat16 *>(c.q);
     a.lens = c.lens; a.lse = c.lse; a.prev = c.prev;
     a.out = c.out;
     a.parts = static_cast<float *>(c.workspace);
     a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.Lq = c.Lq; a.T = c.T; a.block = c.block;
-    a.pc = kTile / a.G < c.Lq ? kTile / a.G : c.Lq;
+    a.pc = 256 / a.G < c.Lq ? 256 / a.G : c.Lq;
     a.nqt = (c.Lq + a.pc - 1) / a.pc;
     a.scale_log2 = c.scale * kLog2e;
     a.decay = c.decay;
