@@ -35,12 +35,12 @@ constexpr int kGroups = 4;             // consumer warpgroups
 constexpr int kConsumers = kGroups * 128;
 constexpr int kThreads = kConsumers + 96;
 constexpr int kTile = 128;             // keys
-constexpr int kMarkChunk = 2048;       // blocks per CTA of the mark kernel
+constexpr int kMarkChunk = 512;        // blocks per CTA of the mark kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightArgs {
     const int32_t *lens;
-    const __nv_bfloat16 *q;
+    const void *q, *k;
     const float *lse, *prev;
     const uint16_t *marks;             // [B, Hkv, nq, nbp] head masks of the kept blocks, or null
     float *out, *parts;                // parts [2 kCtas][kTile]
@@ -538,218 +538,217 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- a few queries
-// Up to 16 query rows per kv-head (decode): a step of tcgen05.mma over 128 keys takes over
-// 100 cycles however few its columns, more than the 1000 a tile's bytes leave, so the
-// scores come from mma.sync: a warp takes 16 keys of a tile as the rows and the queries as
-// 8 or 16 columns, the keys' fragments by ldmatrix from the swizzled tile. A quad of lanes
-// holds a key's row and adds its weights. Two groups of eight warps take the tiles in turn.
-// Bound by HBM: each key is read once.
-constexpr int kFewWarps = 16;
-constexpr int kFewThreads = kFewWarps * 32 + 64;
-constexpr int kFewRing = 196608;         // bytes of key tiles in flight
+// Up to 16 query rows per kv-head (decode), bound by HBM: each key is read once. Neither
+// tcgen05.mma nor TMA pays here: a product step over 128 keys takes over 100 cycles
+// however few its columns (1300 a tile in all, where the tile's bytes leave 1050), and a
+// copy box of a 16-key block some 90 (measured: 185 us, 4.5 TB/s, for a decode step over four
+// 128K caches with mma.sync on TMA tiles). So a warp loads 16 keys straight into the
+// fragments of mma.sync (keys as the 16 rows, queries as 8 or 16 columns): the features of a
+// product step may be taken in any order, as long as keys and queries agree, so a lane's 16
+// bytes of a key serve two steps and a quad reads 64 bytes together. The next 16 keys are
+// on their way meanwhile. A quad holds a key's row and adds its weights. Equal runs of 16-key
+// slabs over all warps.
+constexpr int kSlab = 16;
+constexpr int kFar = 4;                      // slabs ahead that are brought into L2
+constexpr int kFewThreads = 256, kFewCtas = 2 * kCtas;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads, 1)
-    weight_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ WeightArgs a) {
-    constexpr int HALVES = D / 64, K_HALF = kTile * 128, K_SLOT = HALVES * K_HALF, NK = kFewRing / K_SLOT;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full_k[NK], empty_k[NK];
-    __shared__ Pair sh_pair;
-    __shared__ long long sh_total;
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 2); mbar_init(&empty_k[s], kFewWarps / 2); }
-        fence_mbar_init();
-    }
-    if (warp == kFewWarps && lane == 0) prefetch_tmap(&tk);
-    if (warp == 0) {
-        const long long t = run_total(a), pos = (long long)blockIdx.x * run_chunk(t);
-        if (lane == 0) sh_total = t;
-        Pair p = {0, 0, 0, 0, 1, 0};             // a run without a pair: not used
-        if (pos < t) p = locate(a, pos);
-        if (lane == 0) sh_pair = p;
-    }
-    __syncthreads();
+__global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid_constant__ WeightArgs a) {
+    constexpr int KB = D / 32;                   // two product steps (32 features) each
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const int wid = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kFewThreads / 32);
+    const int rows = a.G * a.Lq;
     if (a.marks) asm volatile("griddepcontrol.wait;" ::: "memory");   // the mark kernel's output
-    const long long chunk = run_chunk(sh_total), pos0 = (long long)blockIdx.x * chunk;
-    const int tiles = (int)max(0ll, min(sh_total, pos0 + chunk) - pos0);
-    Pair p = sh_pair;
-
-    if (warp >= kFewWarps) {
-        // ---------------------------------------------------- producers: a part of each tile each
-        const int part = warp - kFewWarps, per = kTile / a.block;
-        int kept = 0, kept_at = -1, nk = 0;      // lane i: kept blocks of key tile kept_at + i
-        bool ok = true;
-        for (int m = 0; m < tiles && ok; ++m) {
-            int want = (1 << per) - 1;
-            if (a.marks && a.nq == 1) {          // blocks that no head keeps are not read
-                if (kept_at < 0 || p.kt >= kept_at + 32 || p.kt == 0) {
-                    kept_at = p.kt;
-                    kept = 0;
-                    const int kt = p.kt + lane;
-                    if (kt < p.nt)
-                        for (int e = 0; e < per; ++e) {
-                            const int j = kt * per + e;
-                            if (j < a.nbp && a.marks[(size_t)p.bg * a.nbp + j]) kept |= 1 << e;
-                        }
-                }
-                want = __shfl_sync(0xffffffffu, kept, p.kt - kept_at);
-            }
-            if (D == 64) want &= part ? 0xaa : 0x55;
-            if (lane == 0) {
-                const int s = m % NK;
-                ok = mbar_wait(&empty_k[s], ((m / NK) & 1) ^ 1, a.err);
-                if (ok) {
-                    mbar_arrive_expect_tx(&full_k[s], (uint32_t)(__popc(want) * a.block * 128));
-                    const int hf = D == 128 ? part : 0, row = p.bg * a.T + p.kt * kTile;
-                    unsigned char *dst = smem + s * K_SLOT + hf * K_HALF;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if ((want >> e) & 1)
-                            tma_load_2d(dst + e * a.block * 128, &tk, &full_k[s], hf * 64, row + e * a.block);
-                    ++nk;
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            bool head;
-            p.next(a, head);
+    // keys behind every sequence: no weight
+    for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
+        const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kSlab - 1) / kSlab * kSlab;
+        if (a.lens && threadIdx.x == 0 && bg % a.Hkv == 0) {
+            const int n = __ldg(a.lens + b);
+            if (n < a.Lq || n > a.T) set_error(a.err, SPA_DEVERR_BAD_COUNT);
         }
-        if (lane == 0) drain_ring<NK>(full_k, nk);
+        for (int t = t0 + threadIdx.x; t < a.T; t += kFewThreads) {
+            const size_t o = (size_t)bg * a.T + t;
+            a.out[o] = a.prev ? a.decay * a.prev[o] : 0.f;
+        }
+    }
+    // this warp's run of slabs
+    auto slabs = [&](int b) -> int { return (seq_len(a, b) + kSlab - 1) / kSlab; };
+    long long total;
+    if (a.lens) {
+        int s = 0;
+        for (int b = lane; b < a.B; b += 32) s += slabs(b);
+        total = (long long)__reduce_add_sync(0xffffffffu, s) * a.Hkv;
     } else {
-        // ---------------------------------------------------- weights
-        const int grp = warp >> 3, slab = warp & 7, gq = lane >> 2, tq = lane & 3;
-        // keys behind every sequence: no weight
-        for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
-            const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kTile - 1) / kTile * kTile;
-            if (a.lens && tid == 0 && bg % a.Hkv == 0) {
-                const int n = __ldg(a.lens + b);
-                if (n < a.Lq || n > a.T) set_error(a.err, SPA_DEVERR_BAD_COUNT);
-            }
-            for (int t = t0 + tid; t < a.T; t += kFewWarps * 32) {
-                const size_t o = (size_t)bg * a.T + t;
-                a.out[o] = a.prev ? a.decay * a.prev[o] : 0.f;
-            }
+        total = (long long)a.B * a.Hkv * slabs(0);
+    }
+    long long pos = total * wid / warps;
+    int left = (int)(total * (wid + 1) / warps - pos);
+    if (left <= 0) return;
+    int b = 0, ns = slabs(0);
+    if (a.lens) {
+        while (pos >= (long long)ns * a.Hkv) {
+            pos -= (long long)ns * a.Hkv;
+            ns = slabs(++b);
         }
-        const int rows = a.G * a.Lq;
-        uint32_t qf[NT][D / 16][2];
-        float nl[NT][2];
-        int ci[NT][2], ch[NT][2];                // position and head of the lane's columns
+    } else {
+        b = (int)(pos / ((long long)ns * a.Hkv));
+        pos -= (long long)b * ns * a.Hkv;
+    }
+    int bg = b * a.Hkv + (int)(pos / ns), sl = (int)(pos % ns), off = seq_len(a, b) - a.Lq;
+
+    // the columns of this lane: position and head
+    int ci[NT][2], ch[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = t * 8 + 2 * tq + e;
-                ch[t][e] = c / a.Lq;
-                ci[t][e] = c - ch[t][e] * a.Lq;
+        for (int e = 0; e < 2; ++e) {
+            const int c = t * 8 + 2 * tq + e;
+            ch[t][e] = c / a.Lq;
+            ci[t][e] = c - ch[t][e] * a.Lq;
+        }
+    const bool one = a.marks && a.nq == 1;       // one list per head: the slab's heads as a mask
+    // head masks of 32 slabs ahead, one per lane
+    uint32_t ahead = 0xffffu;
+    int ahead_at = -1;
+    auto heads_of = [&](int bg_, int s_) -> uint32_t {
+        if (!one) return 0xffffu;
+        if (ahead_at < 0 || s_ < ahead_at || s_ >= ahead_at + 32) {
+            ahead_at = s_;
+            const int blk = (s_ + lane) * kSlab / a.block;
+            ahead = blk < a.nbp ? a.marks[(size_t)bg_ * a.nbp + blk] : 0u;
+        }
+        return __shfl_sync(0xffffffffu, ahead, s_ - ahead_at);
+    };
+    const uint4 *k4 = static_cast<const uint4 *>(a.k);
+    uint4 kr[2][KB][2];                          // [now, next][32 features][keys gq, gq + 8]
+    float pr[2][2];
+    uint32_t hm[2];
+    auto load = [&](int bg_, int s_, uint32_t heads, uint4 (&r)[KB][2], float (&pv)[2]) {
+        const int t = s_ * kSlab + gq;
+        // slabs end inside the cache's rows or are cut at T
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = t + 8 * h < a.T;
+            const size_t row = (size_t)bg_ * a.T + (in ? t + 8 * h : 0);
+            if (heads) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) r[kb][h] = __ldg(k4 + row * (D / 8) + kb * 4 + tq);
             }
-        bool fresh = true, ok = true;
-        for (int m = 0; m < tiles && ok; ++m) {
-            if ((m & 1) == grp) {
-                if (fresh) {                     // a new (b, kv-head): its rows lie together in q and lse
-                    fresh = false;
-                    const size_t row0 = (size_t)p.bg * rows;
-                    const uint32_t *q32 = reinterpret_cast<const uint32_t *>(a.q);
+            pv[h] = a.prev && in && tq == 0 ? a.prev[row] : 0.f;
+        }
+    };
+    uint32_t qf[NT][KB][4];
+    float nl[NT][2];
+    bool fresh = true;
+    hm[0] = heads_of(bg, sl);
+    load(bg, sl, hm[0], kr[0], pr[0]);
+    for (;;) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const bool in = t * 8 + gq < rows;
-                        const uint32_t *qr = q32 + (row0 + (in ? t * 8 + gq : 0)) * (D / 2);
+        for (int now = 0; now < 2; ++now) {      // unrolled so that the two buffers stay registers
+            if (fresh) {                         // a new (b, kv-head): its rows lie together in q and lse
+                fresh = false;
+                const size_t row0 = (size_t)bg * rows;
+                const uint4 *q4 = static_cast<const uint4 *>(a.q);
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            qf[t][ks][0] = in ? __ldg(qr + ks * 8 + tq) : 0u;
-                            qf[t][ks][1] = in ? __ldg(qr + ks * 8 + tq + 4) : 0u;
-                        }
+                for (int t = 0; t < NT; ++t) {
+                    const bool in = t * 8 + gq < rows;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int c = t * 8 + 2 * tq + e;
-                            nl[t][e] = c < rows ? minus_log2(__ldg(a.lse + row0 + c)) : -INFINITY;
-                        }
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const uint4 v = in ? __ldg(q4 + (row0 + t * 8 + gq) * (D / 8) + kb * 4 + tq)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+                        qf[t][kb][0] = v.x;
+                        qf[t][kb][1] = v.y;
+                        qf[t][kb][2] = v.z;
+                        qf[t][kb][3] = v.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = t * 8 + 2 * tq + e;
+                        nl[t][e] = c < rows ? minus_log2(__ldg(a.lse + row0 + c)) : -INFINITY;
                     }
                 }
-                const int t0 = p.kt * kTile + slab * 16 + gq, t1 = t0 + 8;     // the lane's keys
-                const size_t o = (size_t)p.bg * a.T;
-                float b0 = 0.f, b1 = 0.f;
-                if (a.prev && tq == 0) {
-                    if (t0 < a.T) b0 = a.prev[o + t0];
-                    if (t1 < a.T) b1 = a.prev[o + t1];
+            }
+            // the next slab
+            int bg2 = bg, sl2 = sl + 1, off2 = off, ns2 = ns;
+            bool head2 = false;
+            if (left > 1) {
+                if (sl2 >= ns) {
+                    sl2 = 0;
+                    ++bg2;
+                    head2 = true;
+                    ahead_at = -1;
+                    if (bg2 % a.Hkv == 0) {
+                        off2 = seq_len(a, bg2 / a.Hkv) - a.Lq;
+                        ns2 = slabs(bg2 / a.Hkv);
+                    }
                 }
-                // which of its columns see a key: behind it, and kept by the column's head
-                uint32_t see = 0u;                                   // bit 4 t + 2 e + key
-                {
-                    const uint16_t *mk = a.marks ? a.marks + (size_t)p.bg * a.nq * a.nbp : nullptr;
-                    const int blk0 = t0 / a.block, blk1 = t1 / a.block, qb0 = p.off / a.block;
-                    const uint32_t one0 = mk && a.nq == 1 && t0 < a.T ? mk[blk0] : 0xffffu;
-                    const uint32_t one1 = mk && a.nq == 1 && t1 < a.T ? mk[blk1] : 0xffffu;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int at = p.off + ci[t][e];         // the column's position
-                            uint32_t h0 = one0, h1 = one1;
-                            if (mk && a.nq > 1 && ci[t][e] < a.Lq && ch[t][e] < a.G) {
-                                const size_t l = (size_t)(at / a.block - qb0) * a.nbp;
-                                h0 = t0 < a.T ? mk[l + blk0] : 0u;
-                                h1 = t1 < a.T ? mk[l + blk1] : 0u;
-                            }
-                            if (t0 <= at && ((h0 >> ch[t][e]) & 1u)) see |= 1u << (4 * t + 2 * e);
-                            if (t1 <= at && ((h1 >> ch[t][e]) & 1u)) see |= 2u << (4 * t + 2 * e);
-                        }
+                hm[now ^ 1] = heads_of(bg2, sl2);
+                load(bg2, sl2, hm[now ^ 1], kr[now ^ 1], pr[now ^ 1]);
+                // and the slabs after it into L2, a line per lane
+                const int far = sl2 + kFar;
+                if (far < ns2 && (far - sl2) < left) {
+                    const int at = one ? far - ahead_at : 0;
+                    if (at < 32 && (!one || __shfl_sync(0xffffffffu, ahead, at)) && lane < kSlab * D * 2 / 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            reinterpret_cast<const char *>(k4) + (((size_t)bg2 * a.T + far * kSlab) * D * 2 + lane * 128)));
                 }
-                const int s = m % NK;
-                ok = __all_sync(0xffffffffu, mbar_wait(&full_k[s], (m / NK) & 1, a.err));
-                if (!ok) break;
-                const uint32_t kt = smem_u32(smem + s * K_SLOT);
+            }
+            // this one
+            const int t0 = sl * kSlab + gq, t1 = t0 + 8;
+            const size_t o = (size_t)bg * a.T;
+            float w0 = 0.f, w1 = 0.f;
+            if (hm[now]) {
                 float c[NT][2][4];               // two chains per column tile
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) c[t][0][e] = c[t][1][e] = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    // 16 keys x 16 features: rows (lane & 7) + 8 (lane >> 3 & 1), 16-byte chunk by lane >> 4
-                    const int row = slab * 16 + (lane & 15), ck = ks * 2 + (lane >> 4);
-                    const uint32_t addr = kt + (ck >> 3) * K_HALF + row * 128 + (((ck & 7) ^ (row & 7)) << 4);
-                    uint32_t k0, k1, k2, k3;
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(k0), "=r"(k1), "=r"(k2), "=r"(k3) : "r"(addr));
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        asm volatile(
-                            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                            "{%8,%9}, {%0,%1,%2,%3};"
-                            : "+f"(c[t][ks & 1][0]), "+f"(c[t][ks & 1][1]), "+f"(c[t][ks & 1][2]), "+f"(c[t][ks & 1][3])
-                            : "r"(k0), "r"(k1), "r"(k2), "r"(k3), "r"(qf[t][ks][0]), "r"(qf[t][ks][1]));
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty_k[s]);
-                float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 x = kr[now][kb][0], y = kr[now][kb][1];
+                            asm volatile(
+                                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                                "{%8,%9}, {%0,%1,%2,%3};"
+                                : "+f"(c[t][i][0]), "+f"(c[t][i][1]), "+f"(c[t][i][2]), "+f"(c[t][i][3])
+                                : "r"(i ? x.z : x.x), "r"(i ? y.z : y.x), "r"(i ? x.w : x.y), "r"(i ? y.w : y.y),
+                                  "r"(qf[t][kb][2 * i]), "r"(qf[t][kb][2 * i + 1]));
+                        }
+                const uint16_t *mk = a.marks && !one ? a.marks + (size_t)bg * a.nq * a.nbp + sl * kSlab / a.block : nullptr;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const int at = off + ci[t][e];               // the column's position
+                        uint32_t heads = hm[now];
+                        if (mk)
+                            heads = ci[t][e] < a.Lq && ch[t][e] < a.G
+                                        ? mk[(size_t)(at / a.block - off / a.block) * a.nbp] : 0u;
+                        const bool in = (heads >> ch[t][e]) & 1u;
+                        // keys behind the sequence may hold anything: select
                         const float y0 = fmaf(c[t][0][e] + c[t][1][e], a.scale_log2, nl[t][e]);
                         const float y1 = fmaf(c[t][0][2 + e] + c[t][1][2 + e], a.scale_log2, nl[t][e]);
-                        // rows that no copy filled may hold anything: select
-                        w0 += (see >> (4 * t + 2 * e)) & 1u ? fast_exp2(y0) : 0.f;
-                        w1 += (see >> (4 * t + 2 * e)) & 2u ? fast_exp2(y1) : 0.f;
+                        w0 += in && t0 <= at ? fast_exp2(y0) : 0.f;
+                        w1 += in && t1 <= at ? fast_exp2(y1) : 0.f;
                     }
                 w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
                 w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
                 w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
                 w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-                if (tq == 0) {
-                    const int len = p.off + a.Lq;
-                    if (t0 >= len) w0 = 0.f;
-                    if (t1 >= len) w1 = 0.f;
-                    if (t0 < a.T) a.out[o + t0] = a.prev ? fmaf(a.decay, b0, w0) : w0;
-                    if (t1 < a.T) a.out[o + t1] = a.prev ? fmaf(a.decay, b1, w1) : w1;
-                }
             }
-            bool head;
-            p.next(a, head);
-            fresh = fresh || head;
+            if (tq == 0) {
+                if (t0 < a.T) a.out[o + t0] = a.prev ? fmaf(a.decay, pr[now][0], w0) : w0;
+                if (t1 < a.T) a.out[o + t1] = a.prev ? fmaf(a.decay, pr[now][1], w1) : w1;
+            }
+            if (--left == 0) return;
+            bg = bg2;
+            sl = sl2;
+            off = off2;
+            ns = ns2;
+            fresh = head2;
         }
     }
 }
@@ -893,15 +892,11 @@ cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
 
 template <int D, int NT>
 cudaError_t launch_few(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
-    CUtensorMap mq, mk;
-    if (!make_maps(&mq, &mk, c, a.pc)) return cudaErrorNotSupported;
-    constexpr int smem = kFewRing + 1024;
-    const void *kern = reinterpret_cast<const void *>(weight_few_kernel<D, NT>);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const long long most = (long long)c.B * c.Hkv * ((c.T + kTile - 1) / kTile);
-    void *args[] = {&mk, &a};
-    return launch_after(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kFewThreads), smem, args,
+    const long long most = (long long)c.B * c.Hkv * ((c.T + kSlab - 1) / kSlab);
+    const long long ctas = (most + kFewThreads / 32 - 1) / (kFewThreads / 32);
+    void *args[] = {&a};
+    return launch_after(reinterpret_cast<const void *>(weight_few_kernel<D, NT>),
+                        dim3((unsigned)(ctas < kFewCtas ? ctas : kFewCtas)), dim3(kFewThreads), 0, args,
                         a.marks != nullptr, s);
 }
 
@@ -933,7 +928,7 @@ size_t weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block) {
 
 cudaError_t launch_weight(const WeightCall &c, cudaStream_t s) {
     WeightArgs a;
-    a.q = static_cast<const __nv_bfloat16 *>(c.q);
+    a.q = c.q; a.k = c.k;
     a.lens = c.lens; a.lse = c.lse; a.prev = c.prev;
     a.out = c.out;
     a.parts = static_cast<float *>(c.workspace);

@@ -558,8 +558,6 @@ class _On:
 
     def __init__(self, t: torch.Tensor, stream):
         self.dev, self.stream, self.ctx = t.device, stream, None
-        if not t.is_cuda:
-            raise ValueError("libspa works on CUDA tensors only")
 
     def __enter__(self):
         if self.stream is not None:
@@ -577,23 +575,37 @@ class _On:
             self.ctx.__exit__(*exc)
 
 
-def _arg(t: torch.Tensor | None, name: str, shape, dtype, dev) -> int | None:
+def _enqueue(call, t: torch.Tensor, stream):
+    """call(raw stream) on the tensor's device and on `stream`, or the current one."""
+    if not t.is_cuda:
+        raise ValueError("libspa works on CUDA tensors only")
+    dev = t.get_device()
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    with _On(t, stream) as st:
+        return call(st)
+
+
+def _mismatch(t, name, shape, dtype, dev):
+    return ValueError(f"{name} must be {tuple(shape)} {dtype} on cuda:{dev}, "
+                      f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _arg(t: torch.Tensor | None, name: str, shape, dtype, dev: int) -> int | None:
     """The address of a dense tensor of exactly this shape, type and device."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape):
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {dev}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape:
+        raise _mismatch(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _strided(t: torch.Tensor, name: str, shape, dtype, dev):
+def _strided(t: torch.Tensor, name: str, shape, dtype, dev: int):
     """(address, strides or None where dense) of a [B, H, L, d] view with dense rows."""
-    if t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape):
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {dev}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape:
+        raise _mismatch(t, name, shape, dtype, dev)
     if t.is_contiguous():
         return t.data_ptr(), None
     sb, sh, sl, sd = t.stride()
@@ -636,10 +648,12 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
     """Rotates q [B,Hq,L,d] and k [B,Hkv,L,d] (or None) of any strides with dense rows:
     -> (q_out, k_out or None), dense unless given. backward: the transposed rotation."""
     B, Hq, L, d = q.shape
-    dev, dt = q.device, q.dtype
-    with _On(q, stream) as st:
+    dev, dt = q.get_device(), q.dtype
+
+    def call(st):
+        nonlocal q_out, k_out
         if q_out is None:
-            q_out = torch.empty((B, Hq, L, d), device=dev, dtype=dt)
+            q_out = q.new_empty((B, Hq, L, d))
         qp, qs = _strided(q, "q", q.shape, dt, dev)
         qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp = ks = kop = kos = None
@@ -648,7 +662,7 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
             Hkv = k.shape[1]
             shape = (B, Hkv, L, d)
             if k_out is None:
-                k_out = torch.empty(shape, device=dev, dtype=dt)
+                k_out = k.new_empty(shape)
             kp, ks = _strided(k, "k", shape, dt, dev)
             kop, kos = _strided(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
@@ -657,7 +671,9 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
                lib().spa_rope(qp, qs, qop, qos, kp, ks, kop, kos, _dt(q), B, Hq, Hkv, L, d,
                               2 * freqs.numel(), _layout(layout), _rope_freqs(freqs), mscale,
                               _arg(pos, "pos", (B, L), torch.int32, dev), pos0, int(backward), st))
-    return q_out, k_out
+        return q_out, k_out
+
+    return _enqueue(call, q, stream)
 
 
 def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch.Tensor,
@@ -669,10 +685,12 @@ def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch
     rows[b] + t (or row0 + t) of the caches kc, vc [B,Hkv,T,d]."""
     B, Hq, L, d = q.shape
     Hkv, T = kc.shape[1], kc.shape[2]
-    dev, dt = q.device, q.dtype
-    with _On(q, stream) as st:
+    dev, dt = q.get_device(), q.dtype
+
+    def call(st):
+        nonlocal q_out
         if q_out is None:
-            q_out = torch.empty((B, Hq, L, d), device=dev, dtype=dt)
+            q_out = q.new_empty((B, Hq, L, d))
         qp, qs = _strided(q, "q", q.shape, dt, dev)
         qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp, ks = _strided(k, "k", (B, Hkv, L, d), dt, dev)
@@ -684,7 +702,9 @@ def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch
                                      T, d, 2 * freqs.numel(), _layout(layout), _rope_freqs(freqs),
                                      mscale, _arg(pos, "pos", (B, L), torch.int32, dev),
                                      _arg(rows, "rows", (B,), torch.int32, dev), row0, st))
-    return q_out
+        return q_out
+
+    return _enqueue(call, q, stream)
 
 
 def _lists(idx, count, B, Hq, nq, dev):
@@ -715,17 +735,19 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
     for decode or None. Returns (out, lse or None)."""
     B, Hq, n, d = q.shape
     Hkv, T = kc.shape[1], kc.shape[2]
-    dev, dt = q.device, q.dtype
-    with _On(q, stream) as st:
+    dev, dt = q.get_device(), q.dtype
+
+    def call(st):
+        nonlocal workspace, out, lse
         need = spa_tree_workspace_bytes(B, Hq, Hkv, n, T, d, block)
         if workspace is None:
-            workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
-        elif not workspace.is_contiguous() or workspace.device != dev:
+            workspace = q.new_empty((max(need, 16),), dtype=torch.uint8)
+        elif not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
-            out = torch.empty((B, Hq, n, d), device=dev, dtype=dt)
+            out = q.new_empty((B, Hq, n, d))
         if lse is None and want_lse:
-            lse = torch.empty((B, Hq, n), device=dev, dtype=torch.float32)
+            lse = q.new_empty((B, Hq, n), dtype=torch.float32)
         ip, cap, cp = _lists(idx, count, B, Hq, 1, dev)
         _check("spa_sparse_attn_tree",
                lib().spa_sparse_attn_tree(_arg(q, "q", q.shape, dt, dev),
@@ -737,7 +759,9 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
                                           workspace.numel() * workspace.element_size(),
                                           _arg(out, "out", q.shape, dt, dev),
                                           _arg(lse, "lse", (B, Hq, n), torch.float32, dev), st))
-    return out, lse
+        return out, lse
+
+    return _enqueue(call, q, stream)
 
 
 def spa_attn_weight_workspace_bytes(B: int, Hkv: int, Lq: int, T: int, block: int) -> int:
@@ -754,19 +778,21 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
     [B,Hq,Lq], give every key of k [B,Hkv,T,d], added to decay * prev: [B,Hkv,T] fp32."""
     B, Hq, Lq, d = q.shape
     Hkv, T = k.shape[1], k.shape[2]
-    dev, dt = q.device, q.dtype
-    with _On(q, stream) as st:
+    dev, dt = q.get_device(), q.dtype
+
+    def call(st):
+        nonlocal workspace, out
         ip, cap, cp = None, 0, None
         if idx is not None or count is not None:
             nq = (T - 1) // block - (T - Lq) // block + 1 if block > 0 else 0
             ip, cap, cp = _lists(idx, count, B, Hq, nq, dev)
         if workspace is None:
             need = spa_attn_weight_workspace_bytes(B, Hkv, Lq, T, 0 if idx is None else block)
-            workspace = torch.empty((max(need, 16),), device=dev, dtype=torch.uint8)
-        elif not workspace.is_contiguous() or workspace.device != dev:
+            workspace = q.new_empty((max(need, 16),), dtype=torch.uint8)
+        elif not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
-            out = torch.empty((B, Hkv, T), device=dev, dtype=torch.float32)
+            out = q.new_empty((B, Hkv, T), dtype=torch.float32)
         _check("spa_attn_weight",
                lib().spa_attn_weight(_arg(q, "q", q.shape, dt, dev), _arg(k, "k", (B, Hkv, T, d), dt, dev),
                                      _dt(q), B, Hq, Hkv, Lq, T, d,
@@ -775,7 +801,9 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
                                      _arg(prev, "prev", (B, Hkv, T), torch.float32, dev), decay,
                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                      _arg(out, "out", (B, Hkv, T), torch.float32, dev), st))
-    return out
+        return out
+
+    return _enqueue(call, q, stream)
 
 
 def spa_evict_select(score: torch.Tensor, n_keep: int, n_sink: int = 4, n_recent: int = 0,
@@ -784,18 +812,22 @@ def spa_evict_select(score: torch.Tensor, n_keep: int, n_sink: int = 4, n_recent
     """The n_keep keys of score [B,Hkv,T] fp32 that stay: ascending keep [B,Hkv,n_keep] int32
     (-1 behind the last) and count [B] int32."""
     B, Hkv, T = score.shape
-    dev = score.device
-    with _On(score, stream) as st:
+    dev = score.get_device()
+
+    def call(st):
+        nonlocal keep, count
         if keep is None:
-            keep = torch.empty((B, Hkv, max(n_keep, 0)), device=dev, dtype=torch.int32)
+            keep = score.new_empty((B, Hkv, max(n_keep, 0)), dtype=torch.int32)
         if count is None:
-            count = torch.empty((B,), device=dev, dtype=torch.int32)
+            count = score.new_empty((B,), dtype=torch.int32)
         _check("spa_evict_select",
                lib().spa_evict_select(_arg(score, "score", (B, Hkv, T), torch.float32, dev),
                                       _arg(lens, "lens", (B,), torch.int32, dev), B, Hkv, T, n_keep, n_sink,
                                       n_recent, _arg(keep, "keep", (B, Hkv, n_keep), torch.int32, dev),
                                       _arg(count, "count", (B,), torch.int32, dev), st))
-    return keep, count
+        return keep, count
+
+    return _enqueue(call, score, stream)
 
 
 def spa_cache_gather(kc: torch.Tensor, vc: torch.Tensor, keep: torch.Tensor,
@@ -807,16 +839,18 @@ def spa_cache_gather(kc: torch.Tensor, vc: torch.Tensor, keep: torch.Tensor,
     the last, where none are given). Returns (k_out, v_out, score_out or None)."""
     B, Hkv, T, d = kc.shape
     n_keep = keep.shape[2]
-    dev, dt = kc.device, kc.dtype
-    with _On(kc, stream) as st:
-        new = torch.zeros if count is not None else torch.empty
+    dev, dt = kc.get_device(), kc.dtype
+
+    def call(st):
+        nonlocal k_out, v_out, score_out
+        new = kc.new_zeros if count is not None else kc.new_empty
         if k_out is None:
-            k_out = new((B, Hkv, n_keep, d), device=dev, dtype=dt)
+            k_out = new((B, Hkv, n_keep, d))
         T_out = k_out.shape[2]
         if v_out is None:
-            v_out = new((B, Hkv, T_out, d), device=dev, dtype=dt)
+            v_out = new((B, Hkv, T_out, d))
         if score_out is None and score is not None:
-            score_out = new((B, Hkv, T_out), device=dev, dtype=torch.float32)
+            score_out = new((B, Hkv, T_out), dtype=torch.float32)
         _check("spa_cache_gather",
                lib().spa_cache_gather(_arg(kc, "kc", (B, Hkv, T, d), dt, dev),
                                       _arg(vc, "vc", (B, Hkv, T, d), dt, dev),
@@ -826,7 +860,9 @@ def spa_cache_gather(kc: torch.Tensor, vc: torch.Tensor, keep: torch.Tensor,
                                       _arg(k_out, "k_out", (B, Hkv, T_out, d), dt, dev),
                                       _arg(v_out, "v_out", (B, Hkv, T_out, d), dt, dev),
                                       _arg(score_out, "score_out", (B, Hkv, T_out), torch.float32, dev), st))
-    return k_out, v_out, score_out
+        return k_out, v_out, score_out
+
+    return _enqueue(call, kc, stream)
 
 
 def spa_selftest_wait_timeout(limit_us: int, stream=None) -> None:
