@@ -7,6 +7,29 @@
 
 namespace spa {
 
+// Programmatic dependent launch: a kernel launched by launch_early may start while the
+// one before it on the stream still runs (its launch and set-up are hidden), and calls
+// grid_wait before it touches global memory: from there on everything before it is done.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+inline cudaError_t launch_early(const void *kern, dim3 grid, dim3 block, size_t smem, void **args, cudaStream_t s,
+                                unsigned cluster = 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
 constexpr int kRopeMaxPairs = 128;
 
 struct RopeTensor {

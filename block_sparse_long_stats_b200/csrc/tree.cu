@@ -35,7 +35,7 @@ namespace {
 constexpr int kCtas = 148;             // one per SM
 constexpr int kThreads = 352;
 constexpr int kTile = 128;             // keys
-constexpr int kMinTiles = 2;           // tiles a run has at least
+constexpr int kMinTiles = 1;           // tiles a run has at least
 constexpr int kRange = 4096;           // blocks whose list is held in shared memory
 constexpr int kShortList = 1024;       // entries up to which a list is read whole
 constexpr float kLog2e = 1.4426950408889634f;
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tv);
     }
     if (warp == 9) tmem_alloc(&tmem_slot, 512);
+    grid_wait();
     if (warp == 0) {
         const int total = run_total(a), chunk = run_chunk(total);
         if (lane == 0) {
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     const int lane = threadIdx.x & 31, c_lo = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinCols;
     const int unit = blockIdx.x / (RT * 4), srow = blockIdx.x % (RT * 4) * 32 + lane;
     const int bg = unit / a.nrt, b = bg / a.Hkv, row = unit % a.nrt * (RT * 128) + srow;
+    grid_wait();
     const int chunk = run_chunk(run_total(a)), tb = tiles_of(a, b);
     int before = b * tb;
     if (a.lens) {
@@ -745,7 +747,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     const int p0 = before * a.Hkv * a.nrt + (unit - b * a.Hkv * a.nrt) * tb;
     const int c0 = p0 / chunk, ns = (p0 + tb - 1) / chunk - c0 + 1;
     if (ns == 1) return;                        // written by its run
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + ((size_t)c0 + unit) * (RT * 128) + srow;
     const float *src = a.ws_o + (((size_t)c0 + unit) * D + c_lo) * (RT * 128) + srow;
     // online over the runs, four at a time
@@ -809,19 +810,14 @@ cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
     // no more CTAs than runs of kMinTiles tiles (the most that the lengths allow)
     const long long most = (long long)c.B * c.Hkv * a.nrt * ((c.T - c.n + kTile - 1) / kTile + 1);
     const long long ctas = (most + kMinTiles - 1) / kMinTiles;
-    kern<<<(unsigned)(ctas < kCtas ? ctas : kCtas), kThreads, C::SMEM, s>>>(mq, mk, mv, a);
-    e = cudaGetLastError();
+    void *args[] = {&mq, &mk, &mv, &a};
+    e = launch_early(reinterpret_cast<const void *>(kern), dim3((unsigned)(ctas < kCtas ? ctas : kCtas)), dim3(kThreads),
+                     C::SMEM, args, s);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(c.B * c.Hkv * a.nrt * RT * 4), D / (kJoinWarps * kJoinCols));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, RT>, a);
+    void *jargs[] = {&a};
+    return launch_early(reinterpret_cast<const void *>(tree_join_kernel<D, RT>),
+                        dim3((unsigned)(c.B * c.Hkv * a.nrt * RT * 4), D / (kJoinWarps * kJoinCols)),
+                        dim3(kJoinWarps * 32), 0, jargs, s);
 }
 
 template <int D, int RT>

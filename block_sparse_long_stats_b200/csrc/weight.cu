@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tk);
     }
     if (warp == 17) tmem_alloc(&tmem_slot, 512);
+    grid_wait();
     if (warp == 0) {
         const long long t = run_total(a), pos = (long long)blockIdx.x * run_chunk(t);
         if (lane == 0) sh_total = t;
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (a.marks) asm volatile("griddepcontrol.wait;" ::: "memory");   // the mark kernel's output
     const uint32_t tmem = tmem_slot;
     const long long chunk = run_chunk(sh_total), pos0 = (long long)blockIdx.x * chunk;
     const long long jobs = max(0ll, min(sh_total, pos0 + chunk) - pos0);
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
     const int wid = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kFewThreads / 32);
     const int rows = a.G * a.Lq;
-    if (a.marks) asm volatile("griddepcontrol.wait;" ::: "memory");   // the mark kernel's output
+    grid_wait();
     // keys behind every sequence: no weight
     for (int bg = blockIdx.x; bg < a.B * a.Hkv; bg += gridDim.x) {
         const int b = bg / a.Hkv, t0 = (seq_len(a, b) + kSlab - 1) / kSlab * kSlab;
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 // tile that run c begins inside of, if that tile began in run c - 1 or before and no
 // run between begins inside of it too.
 __global__ void __launch_bounds__(kTile) weight_join_kernel(const __grid_constant__ WeightArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const int r = threadIdx.x;
     const long long total = run_total(a), chunk = run_chunk(total);
     const long long pos = (long long)blockIdx.x * chunk;
@@ -787,6 +787,7 @@ __global__ void __launch_bounds__(256) mark_kernel(const int32_t *__restrict__ i
     __shared__ __align__(16) uint16_t mk[kMarkChunk];
     const int unit = blockIdx.x, bg = unit / nq, qb = unit % nq, j_lo = blockIdx.y * kMarkChunk;
     const int j_hi = min(nbp, j_lo + kMarkChunk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int x = threadIdx.x; x < kMarkChunk / 8; x += 256) reinterpret_cast<uint4 *>(mk)[x] = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -857,21 +858,6 @@ bool make_maps(CUtensorMap *mq, CUtensorMap *mk, const WeightCall &c, int pc) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_after(const void *kern, dim3 grid, dim3 block, size_t smem, void **args, bool overlap,
-                         cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelExC(&cfg, kern, args);
-}
-
 template <int D, int NC, bool STREAM>
 cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
     using C = Cfg<D, NC, STREAM>;
@@ -882,12 +868,10 @@ cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const long long most = (long long)c.B * c.Hkv * ((c.T + kTile - 1) / kTile) * a.nqt;
     void *args[] = {&mq, &mk, &a};
-    e = launch_after(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kThreads), C::SMEM, args,
-                     a.marks != nullptr, s);
+    e = launch_early(kern, dim3((unsigned)(most < kCtas ? most : kCtas)), dim3(kThreads), C::SMEM, args, s);
     if (e != cudaSuccess || a.nqt == 1) return e;      // one pair per key tile: no partial sums
     void *jargs[] = {&a};
-    return launch_after(reinterpret_cast<const void *>(weight_join_kernel), dim3(kCtas), dim3(kTile), 0, jargs,
-                        true, s);
+    return launch_early(reinterpret_cast<const void *>(weight_join_kernel), dim3(kCtas), dim3(kTile), 0, jargs, s);
 }
 
 template <int D, int NT>
@@ -895,9 +879,8 @@ cudaError_t launch_few(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
     const long long most = (long long)c.B * c.Hkv * ((c.T + kSlab - 1) / kSlab);
     const long long ctas = (most + kFewThreads / 32 - 1) / (kFewThreads / 32);
     void *args[] = {&a};
-    return launch_after(reinterpret_cast<const void *>(weight_few_kernel<D, NT>),
-                        dim3((unsigned)(ctas < kFewCtas ? ctas : kFewCtas)), dim3(kFewThreads), 0, args,
-                        a.marks != nullptr, s);
+    return launch_early(reinterpret_cast<const void *>(weight_few_kernel<D, NT>),
+                        dim3((unsigned)(ctas < kFewCtas ? ctas : kFewCtas)), dim3(kFewThreads), 0, args, s);
 }
 
 template <int D>
@@ -947,8 +930,11 @@ cudaError_t launch_weight(const WeightCall &c, cudaStream_t s) {
         uint16_t *marks = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(c.workspace) + kPartBytes);
         a.marks = marks;
         const dim3 grid((unsigned)(c.B * c.Hkv * a.nq), (unsigned)((a.nbp + kMarkChunk - 1) / kMarkChunk));
-        mark_kernel<<<grid, 256, 0, s>>>(c.idx, c.count, c.Hkv, a.G, a.nq, nb, a.nbp, c.cap, marks, c.err);
-        const cudaError_t e = cudaGetLastError();
+        int Hkv = c.Hkv, nb_ = nb, cap = c.cap;
+        const int32_t *idx = c.idx, *count = c.count;
+        int *err = c.err;
+        void *args[] = {&idx, &count, &Hkv, &a.G, &a.nq, &nb_, &a.nbp, &cap, &marks, &err};
+        const cudaError_t e = launch_early(reinterpret_cast<const void *>(mark_kernel), grid, dim3(256), 0, args, s);
         if (e != cudaSuccess) return e;
     }
     return c.d == 64 ? launch_d<64>(c, a, s) : launch_d<128>(c, a, s);
