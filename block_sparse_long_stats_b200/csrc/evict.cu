@@ -322,8 +322,7 @@ cudaError_t launch_evict_select(const float *score, const int32_t *lens, int B, 
     const int per = slice(C);
     a.cached = per <= kSliceMax;
     const size_t smem = a.cached ? (size_t)((per + 127) & ~127) * 4 : 0;   // whole steps of 128 keys
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    const cudaError_t e = allow_smem<evict_select_kernel>((size_t)kSliceMax * 4 + 512);
     if (e != cudaSuccess) return e;
     void *args[] = {&a};
     return launch_early(reinterpret_cast<const void *>(evict_select_kernel), dim3((unsigned)((size_t)B * Hkv * C)),

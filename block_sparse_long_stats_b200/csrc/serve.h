@@ -3,6 +3,8 @@
 // these is called.
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 
 namespace spa {
@@ -28,6 +30,20 @@ inline cudaError_t launch_early(const void *kern, dim3 grid, dim3 block, size_t 
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory: set once per kernel and device (one
+// Kern per call site's template arguments keeps the devices that have it).
+template <auto Kern>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev) & 1u) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
 }
 
 constexpr int kRopeMaxPairs = 128;

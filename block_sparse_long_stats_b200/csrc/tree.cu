@@ -4,27 +4,28 @@
 //   out_i = sum_u softmax_u(s q_i.k_u) v_u over the kept cached keys and the ancestors
 //
 // The rows of a problem are the G n queries of a (b, kv-head): they lie next to each
-// other in q, and all of them read the same keys, so K and V cross HBM once for up to
-// 256 rows. Decode with a few drafted tokens is bound by those bytes (512 per key
-// against 4 G n d flops); from about 200 rows on the tensor cores and the exponentials
-// take as long.
+// other in q, and all of them read the same keys. A CTA has 128 of them, a row tile. Decode
+// with a few drafted tokens is bound by the bytes of K and V (512 per key at d = 128 against
+// 4 G n d flops); from about 200 rows on the tensor cores and the exponentials take as long.
 //
 // Work is counted in tiles of 128 keys (kept blocks of the list, closed up; the tree
-// itself is the last tile of its sequence) and the tiles of all (b, kv-head, row tile)
-// units in a row are cut into equal runs, one per CTA and SM, whatever the sequences'
-// lengths: a run may end inside a unit and go on in the next one. A unit that lies in
-// several runs leaves one (m, l, O) state per run in the workspace, and a second kernel
-// joins them.
+// itself is the last tile of its sequence). The tiles of all (b, kv-head) units in a row
+// are cut into equal runs, whatever the sequences' lengths: a run may end inside a unit
+// and go on in the next one. A run is a CTA per row tile; these stand next to each other in
+// the grid and read the same K and V at the same time, so that they cross HBM once. A unit
+// that lies in several runs leaves one (m, l, O) state per run in the workspace, and a
+// second kernel joins them.
 //
-// A CTA has two softmax warpgroups with a score tile S and an output tile O in tensor
-// memory each. With up to 128 rows the warpgroups take the key tiles in turn, each with
-// an own state for all rows, joined at the end (RT = 1); with more rows they work on
-// the same key tile, each for its own 128 rows (RT = 2). Either way one warpgroup's
-// exponentials run beside the other's products. Warp roles:
-//   warps 0-3, 4-7 : softmax; thread r of a warpgroup owns row r = TMEM lane r
-//   warps 8, 10    : TMA producers (Q per unit and a ring of K tiles; a ring of V tiles)
-//   warp 9         : TMEM allocator and tcgen05.mma issuer (one for both warpgroups, which
-//                    so run in turn: with one each 10 % slower)
+// Two CTAs per SM (96 KB of tiles and half of tensor memory each): a CTA's chain of
+// S = Q K^T, softmax, O += P V is serial (P lies over S), and the SM works on one CTA's
+// products and copies during the other's softmax. Warp roles:
+//   warps 0-3 : softmax; thread r owns row r = TMEM lane r
+//   warp 4    : TMA producer (Q per unit; K and V tiles)
+//   warp 5    : TMEM allocator and tcgen05.mma issuer
+// Tried: one CTA per SM with two softmax warpgroups and deeper rings (33 nodes on eight
+// ragged caches 107 us against XX, one or two MMA warps), and halves of 64 keys with a score
+// tile each, so that a warpgroup's softmax overlaps its own products (134 us: a step with
+// N = 64 takes nearly as long as one with N = 128).
 #include <math.h>
 
 #include "serve.h"
@@ -32,11 +33,11 @@
 namespace spa {
 namespace {
 
-constexpr int kCtas = 148;             // one per SM
-constexpr int kThreads = 352;
+constexpr int kCtas = 296;             // two per SM
+constexpr int kThreads = 192;
 constexpr int kTile = 128;             // keys
 constexpr int kMinTiles = 1;           // tiles a run has at least
-constexpr int kRange = 4096;           // blocks whose list is held in shared memory
+constexpr int kRange = 1536;           // blocks whose list is held in shared memory
 constexpr int kShortList = 1024;       // entries up to which a list is read whole
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,22 +47,22 @@ struct TreeArgs {
     const int32_t *parents, *lens, *idx, *count;
     __nv_bfloat16 *out;
     float *lse, *ws_o, *ws_ml;
-    int B, Hq, Hkv, G, n, T, cap, nrt;   // nrt: row tiles per (b, kv-head)
+    int B, Hq, Hkv, G, n, T, cap;
+    int nrt, runs;                       // row tiles per (b, kv-head), runs (CTAs per row tile)
     float scale_log2;
     int *err;
 };
 
-template <int D, int BLK, int RT>
+template <int D, int BLK>
 struct Cfg {
     static constexpr int PER = kTile / BLK;            // blocks per tile
     static constexpr int HALVES = D / 64;              // 64-column halves (128-byte swizzle)
     static constexpr int HALF = kTile * 128;           // bytes of one
-    static constexpr int SLOT = HALVES * HALF;         // a K or V tile, a Q row tile
-    static constexpr int NK = D == 64 ? 4 : (RT == 1 ? 3 : 2);
-    static constexpr int NV = D == 64 ? 4 : 2;
-    static constexpr int OFF_K = RT * SLOT;
-    static constexpr int OFF_V = OFF_K + NK * SLOT;
-    static constexpr int OFF_LIST = OFF_V + NV * SLOT; // uint32 [kRange]: head mask, block
+    static constexpr int SLOT = HALVES * HALF;         // a K or V tile, the Q tile
+    static constexpr int ST = D == 64 ? 2 : 1;         // K and V tiles in flight
+    static constexpr int OFF_K = SLOT;
+    static constexpr int OFF_V = OFF_K + ST * SLOT;
+    static constexpr int OFF_LIST = OFF_V + ST * SLOT; // uint32 [kRange]: head mask, block
     static constexpr int OFF_MARK = OFF_LIST + kRange * 4;   // uint16 [kRange]
     static constexpr int SMEM = OFF_MARK + kRange * 2 + 1024;
     static constexpr uint32_t IDESC_S = idesc_bf16(128, kTile, false);
@@ -80,18 +81,20 @@ __device__ __forceinline__ int tiles_of(const TreeArgs &a, int b) {
 // The runs: tiles in all (below 2^31: the rows of the caches are), tiles per CTA, and
 // where a tile lies. Every lane of a warp calls these together.
 struct Where {
-    int b, unit, t;      // sequence, unit (b-major, then kv-head, then row tile), tile of the unit
+    int b, unit, t;      // sequence, unit (b-major, then kv-head), tile of the unit
 };
 __device__ __forceinline__ int run_total(const TreeArgs &a) {
-    const int lane = threadIdx.x & 31, upb = a.Hkv * a.nrt;
+    const int lane = threadIdx.x & 31, upb = a.Hkv;
     if (!a.lens) return a.B * upb * tiles_of(a, 0);
     int s = 0;
     for (int b = lane; b < a.B; b += 32) s += tiles_of(a, b);
     return __reduce_add_sync(0xffffffffu, s) * upb;
 }
-__device__ __forceinline__ int run_chunk(int total) { return max(kMinTiles, (total + kCtas - 1) / kCtas); }
+__device__ __forceinline__ int run_chunk(const TreeArgs &a, int total) {
+    return max(kMinTiles, (total + a.runs - 1) / a.runs);
+}
 __device__ __forceinline__ Where locate(const TreeArgs &a, int pos) {
-    const int lane = threadIdx.x & 31, upb = a.Hkv * a.nrt;
+    const int lane = threadIdx.x & 31, upb = a.Hkv;
     Where w;
     if (!a.lens) {
         const int tb = tiles_of(a, 0);
@@ -157,61 +160,65 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *x) {
 // needed: the softmax holds 128 scores in registers and has none to spare.
 struct Segment {
     int pos, end;                       // the run's next tile, its end
-    int b, unit, bg, g, P, row0, more;
+    int b, unit, P, more;
     int t_hi, whole, with_tree;         // the unit's tiles end; all of them, the tree here
     int j_hi;                           // blocks of the text end
-    int s_lo, nu, jobs, ntile, tree_here;   // the stretch: first block, kept blocks, jobs, tiles
+    int s_lo, nu, ntile, tree_here;     // the stretch: first block, kept blocks, tiles
     int clean;                          // tiles of PER whole blocks, ahead of the others
-    int tu, done0, done1, segs;         // key tiles, jobs of each warpgroup, segments so far
-    int had;                            // warpgroups with a job in this segment (bits)
+    int tu, segs;                       // key tiles, segments so far
+    int had;                            // key tiles of this segment
 };
 
-template <int D, int BLK, int RT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int BLK>
+__global__ void __launch_bounds__(kThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
-    using C = Cfg<D, BLK, RT>;
-    constexpr int PER = C::PER, NK = C::NK, NV = C::NV;
+    using C = Cfg<D, BLK>;
+    constexpr int PER = C::PER, ST = C::ST;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t *ulist = reinterpret_cast<uint32_t *>(smem + C::OFF_LIST);
     uint16_t *mark = reinterpret_cast<uint16_t *>(smem + C::OFF_MARK);
-    __shared__ uint64_t bar_q, full_k[NK], empty_k[NK], full_v[NV], empty_v[NV], s_full[2],
-        p_ready[2], o_done;
+    __shared__ uint64_t bar_q, full_k[ST], empty_k[ST], full_v[ST], empty_v[ST], s_full, p_ready, o_done;
     __shared__ uint32_t tmem_slot;
     __shared__ Segment sg;
     __shared__ int par[kTile];
     __shared__ uint32_t nmask[kTile][4];          // ancestors and self; all zero: unused
     __shared__ int wcount[kThreads / 32];
-    __shared__ float st_m[2][kTile], st_l[2][kTile];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(&bar_q, 1);
-        for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 1); mbar_init(&empty_k[s], 1); }
-        for (int s = 0; s < NV; ++s) { mbar_init(&full_v[s], 1); mbar_init(&empty_v[s], 1); }
-        for (int w = 0; w < 2; ++w) { mbar_init(&s_full[w], 1); mbar_init(&p_ready[w], 128); }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full_k[s], 1);
+            mbar_init(&empty_k[s], 1);
+            mbar_init(&full_v[s], 1);
+            mbar_init(&empty_v[s], 1);
+        }
+        mbar_init(&s_full, 1);
+        mbar_init(&p_ready, 128);
         mbar_init(&o_done, 1);
         fence_mbar_init();
         fence_async_shared();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 4 && lane == 0) {
         prefetch_tmap(&tq);
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
     }
-    if (warp == 9) tmem_alloc(&tmem_slot, 512);
+    if (warp == 5) tmem_alloc(&tmem_slot, 256);
     grid_wait();
     if (warp == 0) {
-        const int total = run_total(a), chunk = run_chunk(total);
+        const int total = run_total(a), chunk = run_chunk(a, total);
         if (lane == 0) {
-            sg.pos = blockIdx.x * chunk;
+            sg.pos = blockIdx.x / a.nrt * chunk;
             sg.end = min(total, sg.pos + chunk);
-            sg.tu = sg.done0 = sg.done1 = 0;
+            sg.tu = 0;
             sg.segs = -1;
         }
     }
+    const int row0 = blockIdx.x % a.nrt * 128;     // this CTA's rows of every (b, kv-head)
     bool ok = true;                    // cleared by a wait that ran out: no more work, no waits
     tc_fence_before();
     __syncthreads();
@@ -231,10 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int P = text_len(a, w.b), tiles = (P + kTile - 1) / kTile + 1;
                     sg.b = w.b;
                     sg.unit = w.unit;
-                    sg.bg = w.unit / a.nrt;
-                    sg.g = sg.bg % a.Hkv;
                     sg.P = P;
-                    sg.row0 = w.unit % a.nrt * (RT * 128);
                     sg.t_hi = min(tiles, w.t + sg.end - pos);
                     sg.with_tree = sg.t_hi == tiles;
                     sg.whole = w.t == 0 && sg.with_tree;
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.pos = pos + sg.t_hi - w.t;
                     sg.had = 0;
                     ++sg.segs;
-                    if (a.lens && w.unit % (a.Hkv * a.nrt) == 0 && sg.with_tree) {
+                    if (a.lens && w.unit % a.Hkv == 0 && sg.with_tree) {
                         const int p = __ldg(a.lens + w.b);
                         if (p < 0 || p > a.T - a.n) set_error(a.err, SPA_DEVERR_BAD_COUNT);
                     }
@@ -252,14 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
         if (!sg.more) break;
-        if (warp == 8 && lane == 0 && ok) {
-            mbar_arrive_expect_tx(&bar_q, RT * C::SLOT);
-            const int qrow = sg.bg * a.G * a.n + sg.row0;
+        if (warp == 4 && lane == 0 && ok) {
+            mbar_arrive_expect_tx(&bar_q, C::SLOT);
+            const int qrow = sg.unit * a.G * a.n + row0;
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int hf = 0; hf < C::HALVES; ++hf)
-                    tma_load_2d(smem + r * C::SLOT + hf * C::HALF, &tq, &bar_q, hf * 64, qrow + r * 128);
+            for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(smem + hf * C::HALF, &tq, &bar_q, hf * 64, qrow);
         }
         if (tid < a.n) par[tid] = __ldg(a.parents + (size_t)sg.b * a.n + tid);
         if (a.idx)
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         float m_used = -INFINITY, l = 0.f;
-        int started = 0;                             // MMA: warpgroups with a product in O (bits)
+        int started = 0;                             // MMA: a product is in O
         for (;;) {
             // ---------------------------------------- kept blocks of the stretch
             if (a.idx) {
@@ -296,12 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // warps and heads in turn; a list's stretch is found by a 32-way search unless
                 // the whole list is short
                 constexpr int kW = kThreads / 32;
-                const int h_lo = sg.row0 / a.n;
-                const int nh = (min(a.G * a.n, sg.row0 + RT * 128) - 1) / a.n + 1 - h_lo;
+                const int h_lo = row0 / a.n, nh = (min(a.G * a.n, row0 + 128) - 1) / a.n + 1 - h_lo;
                 const int share = max(1, kW / nh);                         // warps per head
                 for (int k = warp; k < nh * share; k += kW) {
                     const int hh = h_lo + k % nh, part = k / nh;
-                    const size_t u = (size_t)sg.bg * a.G + hh;
+                    const size_t u = (size_t)sg.unit * a.G + hh;
                     const int32_t *list = a.idx + u * a.cap;
                     int cnt = __ldg(a.count + u);
                     if (cnt < 0 || cnt > a.cap) {
@@ -372,8 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sg.clean = nu > 0 && nu % PER == 0 && (last_blk + 1) * BLK > sg.P ? nu / PER - 1 : nu / PER;
                 sg.nu = nu;
                 sg.ntile = (nu + PER - 1) / PER + (sg.tree_here ? 1 : 0);
-                sg.jobs = sg.ntile * RT;
-                sg.had |= (sg.jobs > 0 ? 1 : 0) | (sg.jobs > 1 ? 2 : 0);
+                sg.had += sg.ntile;
             }
             __syncthreads();
             const bool last = !a.idx || sg.s_lo + kRange >= sg.j_hi;
@@ -388,16 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return sg.s_lo + (int)(w & 0xffffu);
             };
 
-            if (warp == 8 || warp == 10) {
-                // ------------------------------------ producers
+            if (warp == 4) {
+                // ------------------------------------ producer
                 if (lane == 0 && ok) {
-                    const bool is_v = warp == 10;
-                    const int ns = is_v ? NV : NK, kv_row0 = sg.bg * a.T, ntile = sg.ntile, nu = sg.nu;
-                    uint64_t *full = is_v ? full_v : full_k, *empty = is_v ? empty_v : empty_k;
-                    const CUtensorMap *map = is_v ? &tv : &tk;
-                    unsigned char *ring = smem + (is_v ? C::OFF_V : C::OFF_K);
-                    for (int u = 0; u < ntile; ++u) {
-                        const int tt = sg.tu + u, s = tt % ns;
+                    const int kv_row0 = sg.unit * a.T, ntile = sg.ntile, nu = sg.nu;
+                    for (int u = 0; u < ntile && ok; ++u) {
+                        const int tt = sg.tu + u, s = tt % ST;
                         const bool tree = sg.tree_here && u == ntile - 1;
                         const int nblk = tree ? (a.n + BLK - 1) / BLK : min(PER, nu - u * PER);
                         int rw[PER];                     // read together, ahead of the copies
@@ -406,73 +401,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t hm;
                             rw[e] = kv_row0 + (tree ? sg.P + e * BLK : block_at(min(u * PER + e, nu - 1), hm) * BLK);
                         }
-                        if (!mbar_wait(&empty[s], ((tt / ns) & 1) ^ 1, a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&full[s], (uint32_t)(nblk * BLK * D * 2));
-                        unsigned char *dst = ring + s * C::SLOT;
 #pragma unroll
-                        for (int e = 0; e < PER; ++e)
-                            if (e < nblk) {
-#pragma unroll
-                                for (int hf = 0; hf < C::HALVES; ++hf)
-                                    tma_load_2d(dst + hf * C::HALF + e * BLK * 128, map, &full[s], hf * 64, rw[e]);
+                        for (int kv = 0; kv < 2; ++kv) {
+                            uint64_t *full = kv ? &full_v[s] : &full_k[s];
+                            if (!mbar_wait(kv ? &empty_v[s] : &empty_k[s], ((tt / ST) & 1) ^ 1, a.err)) {
+                                ok = false;
+                                break;
                             }
+                            mbar_arrive_expect_tx(full, (uint32_t)(nblk * BLK * D * 2));
+                            unsigned char *dst = smem + (kv ? C::OFF_V : C::OFF_K) + s * C::SLOT;
+#pragma unroll
+                            for (int e = 0; e < PER; ++e)
+                                if (e < nblk) {
+#pragma unroll
+                                    for (int hf = 0; hf < C::HALVES; ++hf)
+                                        tma_load_2d(dst + hf * C::HALF + e * BLK * 128, kv ? &tv : &tk, full, hf * 64,
+                                                    rw[e]);
+                                }
+                        }
                     }
                 }
-            } else if (warp == 9) {
+            } else if (warp == 5) {
                 // ------------------------------------ products
                 if (lane == 0 && ok) {
-                    const uint32_t tmem = tmem_slot;
-                    const int jobs = sg.jobs, tu = sg.tu, done0 = sg.done0, done1 = sg.done1;
+                    const uint32_t t_s = tmem_slot, qb = smem_u32(smem);
+                    const int ntile = sg.ntile, tu = sg.tu;
                     ok = mbar_wait(&bar_q, sg.segs & 1, a.err);
-                    auto issue_s = [&](int m) -> bool {
-                        const int u = tu + m / RT, w = m & 1, s = u % NK;
-                        if (!mbar_wait(&full_k[s], (u / NK) & 1, a.err)) return false;
+                    auto issue_s = [&](int u) -> bool {
+                        const int s = u % ST;
+                        if (!mbar_wait(&full_k[s], (u / ST) & 1, a.err)) return false;
                         tc_fence_after();
-                        const uint32_t qb = smem_u32(smem + (RT == 2 ? w * C::SLOT : 0));
                         const uint32_t kb = smem_u32(smem + C::OFF_K + s * C::SLOT);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
-                            tc_mma_ss(tmem + w * 256, sw128_desc(qb + off, 16, 1024),
-                                      sw128_desc(kb + off, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
+                            tc_mma_ss(t_s, sw128_desc(qb + off, 16, 1024), sw128_desc(kb + off, 16, 1024),
+                                      C::IDESC_S, kk > 0 ? 1u : 0u);
                         }
-                        tc_commit(&s_full[w]);
-                        if (RT == 1 || w == 1) tc_commit(&empty_k[s]);
+                        tc_commit(&s_full);
+                        tc_commit(&empty_k[s]);
                         return true;
                     };
-                    for (int m = 0; m < 2 && m < jobs && ok; ++m) ok = issue_s(m);
-                    for (int m = 0; m < jobs && ok; ++m) {
-                        const int u = tu + m / RT, w = m & 1, s = u % NV;
-                        ok = mbar_wait(&p_ready[w], ((w ? done1 : done0) + m / 2) & 1, a.err) &&
-                             mbar_wait(&full_v[s], (u / NV) & 1, a.err);
+                    if (ok && ntile > 0) ok = issue_s(tu);
+                    for (int u = tu; u < tu + ntile && ok; ++u) {
+                        const int s = u % ST;
+                        ok = mbar_wait(&p_ready, u & 1, a.err) && mbar_wait(&full_v[s], (u / ST) & 1, a.err);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t vb = smem_u32(smem + C::OFF_V + s * C::SLOT);
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk)
-                            tc_mma_ts(tmem + w * 256 + 128, tmem + w * 256 + kk * 8,
-                                      sw128_desc(vb + kk * 2048, C::HALF, 1024), C::IDESC_O,
-                                      (kk > 0 || ((started >> w) & 1)) ? 1u : 0u);
-                        started |= 1 << w;
-                        if (RT == 1 || w == 1) tc_commit(&empty_v[s]);
-                        if (m + 2 < jobs) ok = issue_s(m + 2);
+                            tc_mma_ts(t_s + 128, t_s + kk * 8, sw128_desc(vb + kk * 2048, C::HALF, 1024), C::IDESC_O,
+                                      (kk > 0 || started) ? 1u : 0u);
+                        started = 1;
+                        tc_commit(&empty_v[s]);
+                        if (u + 1 < tu + ntile) ok = issue_s(u + 1);
                     }
                     if (last && ok) tc_commit(&o_done);
                 }
-            } else if (warp < 8) {
+            } else {
                 // ------------------------------------ softmax
-                const int wg = warp >> 2, r = tid & 127;
-                const int row = sg.row0 + (RT == 2 ? wg * 128 : 0) + r, node = row % a.n, head = row / a.n & 15;
+                const int r = tid, row = row0 + r, node = row % a.n, head = row / a.n & 15;
                 const bool live = row < a.G * a.n &&
                                   (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) != 0u;
                 const bool warp_live = __any_sync(0xffffffffu, live);
-                const uint32_t t_s = tmem_slot + wg * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
-                const int jobs = sg.jobs, clean = sg.clean, kv_tiles = (sg.nu + PER - 1) / PER;
-                for (int m = wg; m < jobs && ok; m += 2) {
-                    const int u = m / RT;
+                const uint32_t t_s = tmem_slot + ((uint32_t)(warp * 32) << 16), t_o = t_s + 128;
+                const int ntile = sg.ntile, tu = sg.tu, clean = sg.clean, kv_tiles = (sg.nu + PER - 1) / PER;
+                for (int u = 0; u < ntile && ok; ++u) {
                     // in a clean tile this row's head keeps a block whole or not at all (bit e)
                     const bool tree = u >= kv_tiles, dirty = u >= clean;
                     uint32_t kept = (1u << PER) - 1u;
@@ -492,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!live) kept = (1u << PER) - 1u;         // an unused row: anything
                     }
                     // (votes: a warp gives up as one)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&s_full[wg], ((wg ? sg.done1 : sg.done0) + m / 2) & 1, a.err));
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full, (tu + u) & 1, a.err));
                     if (!ok) break;
                     tc_fence_after();
                     // rows of V that no key of this sequence fills (behind the text, blocks
@@ -508,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t hm;
                             fill = k >= sg.nu || block_at(k, hm) * BLK + r % BLK >= sg.P;
                         }
-                        const int tt = sg.tu + u, s = tt % NV;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&full_v[s], (tt / NV) & 1, a.err));
+                        const int tt = tu + u, s = tt % ST;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&full_v[s], (tt / ST) & 1, a.err));
                         if (!ok) break;
                         if (fill) {
                             unsigned char *vr = smem + C::OFF_V + s * C::SLOT + r * 128;
@@ -578,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rescale = l > 0.f;
                             m_used = mx;
                         }
-                        // this warpgroup's previous P V completed before S(m) did: O is stable
+                        // the previous P V completed before S did: O is stable
                         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
@@ -617,14 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_wait_st();
                     }
                     tc_fence_before();
-                    mbar_arrive(&p_ready[wg]);
+                    mbar_arrive(&p_ready);
                 }
             }
             __syncthreads();
             if (tid == 0) {
                 sg.tu += sg.ntile;
-                sg.done0 += (sg.jobs + 1) / 2;
-                sg.done1 += sg.jobs / 2;
             }
             if (last) break;
             if (tid == 0) sg.s_lo += kRange;
@@ -633,77 +625,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ------------------------------------------------ the segment's state
-        if (warp < 8) {
-            const int wg = warp >> 2, r = tid & 127;
-            const int row = sg.row0 + (RT == 2 ? wg * 128 : 0) + r;
-            {                                            // an unused row: no key
-                const int node = row % a.n;
-                if (row >= a.G * a.n || (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) == 0u) {
-                    m_used = -INFINITY;
-                    l = 0.f;
-                }
-            }
-            st_m[wg][r] = m_used;
-            st_l[wg][r] = l;
-            named_bar_sync(1, 256);
-            if (ok) ok = mbar_wait(&o_done, sg.segs & 1, a.err);
-            ok = __all_sync(0xffffffffu, ok);
+        if (warp < 4) {
+            const int r = tid, row = row0 + r, node = row % a.n;
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_done, sg.segs & 1, a.err));
             tc_fence_after();
-            // RT = 1: both warpgroups hold a state of every row; each joins half of the
-            // columns. RT = 2: the row's only state.
-            float m_all = m_used, f0 = 1.f, f1 = 0.f, l_all = l;
-            if (RT == 1) {
-                m_all = fmaxf(st_m[0][r], st_m[1][r]);
-                const float mb = m_all == -INFINITY ? 0.f : m_all;
-                f0 = fast_exp2(st_m[0][r] - mb);
-                f1 = fast_exp2(st_m[1][r] - mb);
-                l_all = st_l[0][r] * f0 + st_l[1][r] * f1;
-            }
-            const bool use0 = ok && (RT == 2 ? ((sg.had >> wg) & 1) && l > 0.f : (sg.had & 1) && st_l[0][r] > 0.f);
-            const bool use1 = ok && RT == 1 && (sg.had & 2) && st_l[1][r] > 0.f;
-            constexpr int COLS = RT == 1 ? D / 2 : D;
-            const int c_lo = RT == 1 ? wg * COLS : 0;
-            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t t_o0 = tmem_slot + (RT == 2 ? wg * 256 : 0) + 128 + lane_off;
-            const uint32_t t_o1 = tmem_slot + 256 + 128 + lane_off;
-            const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
             const bool store = row < a.G * a.n, whole = sg.whole;
-            const size_t orow = (size_t)sg.bg * a.G * a.n + row;
-            const size_t slot = (size_t)blockIdx.x + sg.unit;    // of this run's state of this unit
-            const int srow = row - sg.row0;
+            if (!store || (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) == 0u) {
+                m_used = -INFINITY;                      // an unused row: no key
+                l = 0.f;
+            }
+            const bool use = ok && sg.had > 0 && l > 0.f;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const uint32_t t_o = tmem_slot + 128 + ((uint32_t)(warp * 32) << 16);
+            const size_t orow = (size_t)sg.unit * a.G * a.n + row;
+            // the state of this run and unit, this row tile: [D][128], a warp's rows side by side
+            const size_t slot = ((size_t)(blockIdx.x / a.nrt) + sg.unit) * a.nrt + blockIdx.x % a.nrt;
             if (__any_sync(0xffffffffu, store)) {
 #pragma unroll 1
-                for (int c = 0; c < COLS; c += 32) {
-                    float o[32], v[32];
-                    tmem_ld32f(t_o0 + c_lo + c, o);
-                    if (RT == 1) tmem_ld32f(t_o1 + c_lo + c, v);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32f(t_o + c, o);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        o[e] = use0 ? o[e] * f0 : 0.f;
-                        if (RT == 1) o[e] += use1 ? v[e] * f1 : 0.f;
-                    }
+                    for (int e = 0; e < 32; ++e) o[e] = use ? o[e] : 0.f;
                     if (!store) continue;
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c_lo + c);
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             dst[e / 8] = make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
                                                     pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
                                                     pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
                                                     pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
-                    } else {                              // [D][rows]: a warp's rows side by side
-                        float *dst = a.ws_o + (slot * D + c_lo + c) * (RT * 128) + srow;
+                    } else {
+                        float *dst = a.ws_o + (slot * D + c) * 128 + r;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) dst[e * (RT * 128)] = o[e];
+                        for (int e = 0; e < 32; ++e) dst[e * 128] = o[e];
                     }
                 }
             }
-            if (store && (RT == 2 || wg == 0)) {
+            if (store) {
                 if (whole) {
-                    if (a.lse) a.lse[orow] = l_all > 0.f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+                    if (a.lse) a.lse[orow] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
                 } else {
-                    reinterpret_cast<float2 *>(a.ws_ml)[slot * (RT * 128) + srow] = make_float2(m_all, l_all);
+                    reinterpret_cast<float2 *>(a.ws_ml)[slot * 128 + r] = make_float2(m_used, l);
                 }
             }
             tc_fence_before();
@@ -712,31 +677,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
     }
     // copies still in flight on a failure path land before the CTA leaves
-    if ((warp == 8 || warp == 10) && lane == 0) {
-        if (warp == 8 && sg.segs >= 0) mbar_drain(&bar_q, sg.segs & 1);
+    if (warp == 4 && lane == 0) {
+        if (sg.segs >= 0) mbar_drain(&bar_q, sg.segs & 1);
         if (!ok) {
-            if (warp == 8) drain_ring<NK>(full_k, sg.tu);
-            else drain_ring<NV>(full_v, sg.tu);
+            drain_ring<ST>(full_k, sg.tu);
+            drain_ring<ST>(full_v, sg.tu);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem_slot, 512);
+        tmem_dealloc(tmem_slot, 256);
     }
 }
 
 // Joins the states of the units that lie in several runs. A CTA has 32 rows of a unit, one
 // per lane, and 32 features, four per warp.
 constexpr int kJoinWarps = 8, kJoinCols = 4;
-template <int D, int RT>
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
     const int lane = threadIdx.x & 31, c_lo = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinCols;
-    const int unit = blockIdx.x / (RT * 4), srow = blockIdx.x % (RT * 4) * 32 + lane;
-    const int bg = unit / a.nrt, b = bg / a.Hkv, row = unit % a.nrt * (RT * 128) + srow;
+    const int unit = blockIdx.x / (a.nrt * 4), rt = blockIdx.x / 4 % a.nrt, srow = blockIdx.x % 4 * 32 + lane;
+    const int b = unit / a.Hkv, row = rt * 128 + srow;
     grid_wait();
-    const int chunk = run_chunk(run_total(a)), tb = tiles_of(a, b);
+    const int chunk = run_chunk(a, run_total(a)), tb = tiles_of(a, b);
     int before = b * tb;
     if (a.lens) {
         before = 0;
@@ -744,11 +709,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
         before = __reduce_add_sync(0xffffffffu, before);
     }
     if (row >= a.G * a.n) return;
-    const int p0 = before * a.Hkv * a.nrt + (unit - b * a.Hkv * a.nrt) * tb;
+    const int p0 = before * a.Hkv + (unit - b * a.Hkv) * tb;
     const int c0 = p0 / chunk, ns = (p0 + tb - 1) / chunk - c0 + 1;
     if (ns == 1) return;                        // written by its run
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + ((size_t)c0 + unit) * (RT * 128) + srow;
-    const float *src = a.ws_o + (((size_t)c0 + unit) * D + c_lo) * (RT * 128) + srow;
+    const size_t slot0 = ((size_t)c0 + unit) * a.nrt + rt, step = a.nrt;   // a run further: nrt slots
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + slot0 * 128 + srow;
+    const float *src = a.ws_o + (slot0 * D + c_lo) * 128 + srow;
     // online over the runs, four at a time
     float M = -INFINITY, L = 0.f, o[kJoinCols] = {0.f, 0.f, 0.f, 0.f};
     for (int s0 = 0; s0 < ns; s0 += 4) {
@@ -757,11 +723,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const bool in = s0 + k < ns;
-            const size_t at = in ? s0 + k : 0;
-            st[k] = ml[at * (RT * 128)];
+            const size_t at = in ? (s0 + k) * step : 0;
+            st[k] = ml[at * 128];
             if (!in) st[k].x = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < kJoinCols; ++e) v[k][e] = src[(at * D + e) * (RT * 128)];
+            for (int e = 0; e < kJoinCols; ++e) v[k][e] = src[(at * D + e) * 128];
         }
         const float mn = fmaxf(fmaxf(M, fmaxf(st[0].x, st[1].x)), fmaxf(st[2].x, st[3].x));
         const float mb = mn == -INFINITY ? 0.f : mn, f = fast_exp2(M - mb);
@@ -778,7 +744,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
         M = mn;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    const size_t orow = (size_t)bg * a.G * a.n + row;
+    const size_t orow = (size_t)unit * a.G * a.n + row;
     *reinterpret_cast<uint2 *>(a.out + orow * D + c_lo) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
     if (a.lse && c_lo == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
@@ -796,50 +762,46 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t rows, int d, int box_
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int BLK, int RT>
+template <int D, int BLK>
 cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
-    using C = Cfg<D, BLK, RT>;
+    using C = Cfg<D, BLK>;
     CUtensorMap mq, mk, mv;
     const uint64_t kv_rows = (uint64_t)c.B * c.Hkv * c.T;
     if (!make_map(&mq, c.q, (uint64_t)c.B * c.Hq * c.n, D, 128) || !make_map(&mk, c.kc, kv_rows, D, BLK) ||
         !make_map(&mv, c.vc, kv_rows, D, BLK))
         return cudaErrorNotSupported;
-    auto kern = tree_kernel<D, BLK, RT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = allow_smem<tree_kernel<D, BLK>>(C::SMEM);
     if (e != cudaSuccess) return e;
     // no more CTAs than runs of kMinTiles tiles (the most that the lengths allow)
-    const long long most = (long long)c.B * c.Hkv * a.nrt * ((c.T - c.n + kTile - 1) / kTile + 1);
-    const long long ctas = (most + kMinTiles - 1) / kMinTiles;
+    const long long most = (long long)c.B * c.Hkv * ((c.T - c.n + kTile - 1) / kTile + 1);
+    const long long runs = (most + kMinTiles - 1) / kMinTiles;
     void *args[] = {&mq, &mk, &mv, &a};
-    e = launch_early(reinterpret_cast<const void *>(kern), dim3((unsigned)(ctas < kCtas ? ctas : kCtas)), dim3(kThreads),
-                     C::SMEM, args, s);
+    e = launch_early(reinterpret_cast<const void *>(tree_kernel<D, BLK>),
+                     dim3((unsigned)((runs < a.runs ? runs : a.runs) * a.nrt)), dim3(kThreads), C::SMEM, args, s);
     if (e != cudaSuccess) return e;
     void *jargs[] = {&a};
-    return launch_early(reinterpret_cast<const void *>(tree_join_kernel<D, RT>),
-                        dim3((unsigned)(c.B * c.Hkv * a.nrt * RT * 4), D / (kJoinWarps * kJoinCols)),
-                        dim3(kJoinWarps * 32), 0, jargs, s);
+    return launch_early(reinterpret_cast<const void *>(tree_join_kernel<D>),
+                        dim3((unsigned)(c.B * c.Hkv * a.nrt * 4), D / (kJoinWarps * kJoinCols)), dim3(kJoinWarps * 32),
+                        0, jargs, s);
 }
 
-template <int D, int RT>
+template <int D>
 cudaError_t launch_d(const TreeCall &c, const TreeArgs &a, cudaStream_t s) {
     // without lists the keys are read 128 at a time, whatever the block
     switch (c.idx ? c.block : kTile) {
-        case 16: return launch_cfg<D, 16, RT>(c, a, s);
-        case 32: return launch_cfg<D, 32, RT>(c, a, s);
-        case 64: return launch_cfg<D, 64, RT>(c, a, s);
-        default: return launch_cfg<D, 128, RT>(c, a, s);
+        case 16: return launch_cfg<D, 16>(c, a, s);
+        case 32: return launch_cfg<D, 32>(c, a, s);
+        case 64: return launch_cfg<D, 64>(c, a, s);
+        default: return launch_cfg<D, 128>(c, a, s);
     }
 }
 
-// Rows that a CTA handles: 128, or 256 where there are more.
-int row_tiles(int G, int n, int &per) {
-    per = G * n > 128 ? 256 : 128;
-    return (G * n + per - 1) / per;
-}
+// Row tiles per (b, kv-head), and the runs that leaves.
+int row_tiles(int G, int n) { return (G * n + 127) / 128; }
+int runs_of(int nrt) { return kCtas / nrt; }
 size_t state_rows(int B, int Hq, int Hkv, int n) {
-    int per;
-    const int nrt = row_tiles(Hq / Hkv, n, per);
-    return ((size_t)kCtas + (size_t)B * Hkv * nrt) * per;
+    const int nrt = row_tiles(Hq / Hkv, n);
+    return ((size_t)runs_of(nrt) + (size_t)B * Hkv) * nrt * 128;
 }
 
 }  // namespace
@@ -857,12 +819,11 @@ cudaError_t launch_tree(const TreeCall &c, cudaStream_t s) {
     a.ws_o = static_cast<float *>(c.workspace);
     a.ws_ml = a.ws_o + state_rows(c.B, c.Hq, c.Hkv, c.n) * c.d;
     a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.n = c.n; a.T = c.T; a.cap = c.cap;
-    int per;
-    a.nrt = row_tiles(a.G, a.n, per);
+    a.nrt = row_tiles(a.G, a.n);
+    a.runs = runs_of(a.nrt);
     a.scale_log2 = c.scale * kLog2e;
     a.err = c.err;
-    if (c.d == 64) return per == 256 ? launch_d<64, 2>(c, a, s) : launch_d<64, 1>(c, a, s);
-    return per == 256 ? launch_d<128, 2>(c, a, s) : launch_d<128, 1>(c, a, s);
+    return c.d == 64 ? launch_d<64>(c, a, s) : launch_d<128>(c, a, s);
 }
 
 }  // namespace spa

@@ -864,7 +864,7 @@ cudaError_t launch_cfg(const WeightCall &c, WeightArgs &a, cudaStream_t s) {
     CUtensorMap mq, mk;
     if (!make_maps(&mq, &mk, c, a.pc)) return cudaErrorNotSupported;
     const void *kern = reinterpret_cast<const void *>(weight_kernel<D, NC, STREAM>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = allow_smem<weight_kernel<D, NC, STREAM>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const long long most = (long long)c.B * c.Hkv * ((c.T + kTile - 1) / kTile) * a.nqt;
     void *args[] = {&mq, &mk, &a};

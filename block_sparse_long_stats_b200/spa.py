@@ -8,6 +8,7 @@ tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -653,7 +654,7 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
     def call(st):
         nonlocal q_out, k_out
         if q_out is None:
-            q_out = q.new_empty((B, Hq, L, d))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qp, qs = _strided(q, "q", q.shape, dt, dev)
         qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp = ks = kop = kos = None
@@ -662,7 +663,7 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
             Hkv = k.shape[1]
             shape = (B, Hkv, L, d)
             if k_out is None:
-                k_out = k.new_empty(shape)
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
             kp, ks = _strided(k, "k", shape, dt, dev)
             kop, kos = _strided(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
@@ -690,7 +691,7 @@ def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch
     def call(st):
         nonlocal q_out
         if q_out is None:
-            q_out = q.new_empty((B, Hq, L, d))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qp, qs = _strided(q, "q", q.shape, dt, dev)
         qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp, ks = _strided(k, "k", (B, Hkv, L, d), dt, dev)
@@ -720,6 +721,7 @@ def _lists(idx, count, B, Hq, nq, dev):
             _arg(count, "count", (B, Hq, nq), torch.int32, dev))
 
 
+@functools.lru_cache(maxsize=256)
 def spa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, n: int, T: int, d: int, block: int) -> int:
     return int(lib().spa_tree_workspace_bytes(B, Hq, Hkv, n, T, d, block))
 
@@ -745,7 +747,7 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
         elif not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
-            out = q.new_empty((B, Hq, n, d))
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if lse is None and want_lse:
             lse = q.new_empty((B, Hq, n), dtype=torch.float32)
         ip, cap, cp = _lists(idx, count, B, Hq, 1, dev)
@@ -764,6 +766,7 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
     return _enqueue(call, q, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def spa_attn_weight_workspace_bytes(B: int, Hkv: int, Lq: int, T: int, block: int) -> int:
     return int(lib().spa_attn_weight_workspace_bytes(B, Hkv, Lq, T, block))
 
