@@ -53,7 +53,7 @@ spa_status check_rope(const RopeCall &c, spa_dtype dt, int Hq, int Hkv, spa_rope
             return fail(SPA_ERR_INVALID, "tensors must be aligned to their elements");
     if (c.d > 2 * kRopeMaxPairs) return fail(SPA_ERR_UNSUPPORTED, "d must be at most 256");
     if ((long long)Hq + 2ll * Hkv > 65535) return fail(SPA_ERR_UNSUPPORTED, "too many heads");
-    if ((long long)c.B * c.L > (1ll << 31)) return fail(SPA_ERR_UNSUPPORTED, "too many tokens");
+    if ((long long)c.B * c.L > (1ll << 30)) return fail(SPA_ERR_UNSUPPORTED, "too many tokens");
     return SPA_OK;
 }
 
@@ -230,6 +230,9 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
     if (Hq / Hkv > 16) return fail(SPA_ERR_UNSUPPORTED, "at most 16 query heads per kv-head");
     if ((long long)B * Hkv * T > 0x7fffffffll || (long long)B * Hq * Lq > 0x7fffffffll || B * (long long)Hkv > 65535)
         return fail(SPA_ERR_UNSUPPORTED, "too many rows");
+    // (128-key tile, query tile of at least 16 positions) pairs per CTA: a 32-bit count
+    if (((long long)B * Hkv * T / 128 + 1) * (Lq / 16ll + 1) / 148 > 0x7fffffffll)
+        return fail(SPA_ERR_UNSUPPORTED, "too many queries and keys");
     if (idx) {
         if (block <= 0) return fail(SPA_ERR_INVALID, "sizes must be positive");
         if (!block_ok(block)) return fail(SPA_ERR_UNSUPPORTED, "block must be 16, 32, 64 or 128");

@@ -35,6 +35,7 @@ constexpr int kGroups = 4;             // consumer warpgroups
 constexpr int kConsumers = kGroups * 128;
 constexpr int kThreads = kConsumers + 96;
 constexpr int kTile = 128;             // keys
+constexpr int kUnits = 8;              // key tiles that warpgroups may be apart by, and more
 constexpr int kMarkChunk = 512;        // blocks per CTA of the mark kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -214,13 +215,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Pair sh_pair;
     __shared__ long long sh_total;
     __shared__ __align__(16) float nl_s[kGroups][COLS]; // -lse of the columns, log2 units
-    __shared__ float red[2][kGroups][kTile];
+    __shared__ float red[STREAM ? kUnits : 1][kGroups][kTile];   // sums of the last key tiles
+    __shared__ int arrived[STREAM ? kUnits : 1][4];              // warps that have brought theirs
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < NK; ++s) { mbar_init(&full_k[s], 2); mbar_init(&empty_k[s], 1); }
         for (int s = 0; s < NQ; ++s) { mbar_init(&full_q[s], 1); mbar_init(&empty_q[s], 1); }
         for (int w = 0; w < BUFS; ++w) { mbar_init(&s_full[w], 1); mbar_init(&s_empty[w], 128 * C::SHARE); }
+        for (int w = 0; STREAM && w < kUnits * 4; ++w) arrived[w >> 2][w & 3] = 0;
         fence_mbar_init();
     }
     // query rows that no copy fills stay zero (finite scores; their columns count nothing)
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const long long chunk = run_chunk(sh_total), pos0 = (long long)blockIdx.x * chunk;
-    const long long jobs = max(0ll, min(sh_total, pos0 + chunk) - pos0);
+    const int jobs = (int)max(0ll, min(sh_total, pos0 + chunk) - pos0);   // below 2^31: checked by the API
     const bool gq1 = a.nq == 1;
 
     if (warp == 16 || warp == 18) {
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool new_k = true, new_q = true;
         const int per = kTile / a.block;
         int kept = 0, kept_at = -1;      // lane i: kept blocks of key tile kept_at + i
-        for (long long m = 0; m < jobs && ok; ++m) {
+        for (int m = 0; m < jobs && ok; ++m) {
             if (new_q && lane == 0 && part == 0) {
                 const int s = nqs % NQ;
                 ok = mbar_wait(&empty_q[s], ((nqs / NQ) & 1) ^ 1, a.err);
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true, new_k = true, new_q = true;
             int nk = 0, nqs = 0;
             Pair p = sh_pair;
-            for (long long m = 0; m < jobs && ok; m += TWO) {
+            for (int m = 0; m < jobs && ok; m += TWO) {
                 uint32_t kb[TWO], qb[TWO];
                 int k_used[TWO], q_used[TWO], free_q[TWO];
                 const int n = TWO == 1 || m + 1 == jobs ? 1 : 2;
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < TWO; ++i)
                         if (i < n)
-                            tc_mma_ss(tmem + (int)((m + i) % BUFS) * (512 / BUFS), sw128_desc(kb[i] + ko, 16, 1024),
+                            tc_mma_ss(tmem + (m + i) % BUFS * (512 / BUFS), sw128_desc(kb[i] + ko, 16, 1024),
                                       sw128_desc(qb[i] + qo, 16, 1024), C::IDESC, kk > 0 ? 1u : 0u);
                 }
 #pragma unroll
@@ -405,10 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, fresh = true;          // fresh: this group's columns changed
         float sum = 0.f;
         int units = 0;
-        long long unit_first = 0;              // the key tile's first pair in this run
+        int unit_first = 0;                    // the key tile's first pair in this run
         const int first_qi = jobs > 0 ? first_tile(a, p.kt, p.off) : 0;
         bool from_start = jobs > 0 && p.qi == first_qi;
-        for (long long m = 0; m < jobs; ++m) {
+        for (int m = 0; m < jobs; ++m) {
             const bool mine = m % BUFS == buf;
             const int t = p.kt * kTile + r;
             const size_t o = (size_t)p.bg * a.T + t;
@@ -506,19 +509,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (STREAM && (last_pair || m + 1 == jobs)) {
-                // the key tile's sum over the groups, in their order
-                red[units & 1][wg][r] = sum;
+                // The key tile's sum over the groups: each brings its own, and of the four warps
+                // with the same keys the last one adds them up, in the groups' order. No group
+                // waits for another; the score tiles keep them within four jobs.
+                const int slot = units % kUnits, rows32 = warp & 3;
+                red[slot][wg][r] = sum;
                 sum = 0.f;
-                named_bar_sync(1, kConsumers);
-                if ((units & (kGroups - 1)) == wg && t < a.T) {
+                __threadfence_block();
+                __syncwarp();
+                int before = 0;
+                if (lane == 0) before = atomicAdd(&arrived[slot][rows32], 1);
+                if (__shfl_sync(0xffffffffu, before, 0) == kGroups - 1) {
+                    __threadfence_block();
+                    if (lane == 0) arrived[slot][rows32] = 0;
                     float s = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kGroups; ++w) s += red[units & 1][w][r];
+                    for (int w = 0; w < kGroups; ++w) s += *reinterpret_cast<volatile float *>(&red[slot][w][r]);
                     if (t >= p.off + a.Lq) s = 0.f;
-                    if (from_start && last_pair)
-                        a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
-                    else
-                        a.parts[((size_t)blockIdx.x * 2 + (unit_first > 0 ? 1 : 0)) * kTile + r] = s;
+                    if (t < a.T) {
+                        if (from_start && last_pair)
+                            a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
+                        else
+                            a.parts[((size_t)blockIdx.x * 2 + (unit_first > 0 ? 1 : 0)) * kTile + r] = s;
+                    }
                 }
                 ++units;
                 unit_first = m + 1;
