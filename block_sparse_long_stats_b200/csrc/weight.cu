@@ -474,21 +474,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c0 = 0; c0 < COLS; c0 += 16) {
                         tc_wait_ld();
-                        const float *y = x[(c0 / 16) & 1];
+                        float *y = x[(c0 / 16) & 1];
                         if (c0 + 16 < COLS) tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
-                        const uint32_t bits = masked ? see[c0 >> 5] >> (c0 & 16) : 0xffffu;
+                        // a key no one keeps may hold anything: select (few tiles have a mask:
+                        // __any_sync keeps this a branch; as selects it took as long as the sums)
+                        if (__any_sync(0xffffffffu, masked)) {
+                            const uint32_t bits = see[c0 >> 5] >> (c0 & 16);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             const float4 n4 = *reinterpret_cast<const float4 *>(&nl_s[wg][c0 + e]);
                             float y0, y1, y2, y3;
                             f32x2_split(fma_f32x2(f32x2(y[e], y[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
                             f32x2_split(fma_f32x2(f32x2(y[e + 2], y[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
-                            if (masked) {          // a key no one keeps may hold anything: select
-                                y0 = (bits >> e) & 1u ? y0 : -INFINITY;
-                                y1 = (bits >> (e + 1)) & 1u ? y1 : -INFINITY;
-                                y2 = (bits >> (e + 2)) & 1u ? y2 : -INFINITY;
-                                y3 = (bits >> (e + 3)) & 1u ? y3 : -INFINITY;
-                            }
                             acc[0] = add_f32x2(acc[0], f32x2(fast_exp2(y0), fast_exp2(y1)));
                             acc[1] = add_f32x2(acc[1], f32x2(fast_exp2(y2), fast_exp2(y3)));
                         }
