@@ -232,6 +232,8 @@ SCALE = {64: 0.125, 128: 128.0 ** -0.5}
     (5, 4, 4, 2, 4097, 128, 32, 0.9, True),
     (1, 8, 1, 16, 9000, 128, 16, 0.4, False),
     (1, 8, 1, 17, 6000, 64, 128, None, False),
+    (40, 8, 4, 3, 150, 64, 32, 0.5, True),            # more sequences than lanes, many units a run
+    (3, 16, 8, 2, 2, 128, 16, None, False),           # a tree that fills the cache
 ])
 def test_tree_matches_fp64(B, Hq, Hkv, n, T, d, block, p, ragged):
     g = gen(T + n)
@@ -254,6 +256,69 @@ def test_tree_matches_fp64(B, Hq, Hkv, n, T, d, block, p, ragged):
     check_tree(q, kc, vc, parents, block, keep, SCALE[d], lens, out, lse)
     again, _ = spa.spa_sparse_attn_tree(q, kc, vc, parents, block, idx, count, SCALE[d], lens=lens)
     assert torch.equal(again, out)
+
+
+def test_tree_lists_longer_than_a_stretch():
+    # 2048 rows leave few runs: each walks over several stretches of its long lists
+    g = gen(13)
+    G, n, T, block = 16, 128, 450000, 16
+    q, kc, vc = randn(g, 1, G, n, 128), randn(g, 1, 1, T, 128), randn(g, 1, 1, T, 128)
+    parents = tree_of(g, 1, n)
+    idx, count, keep = lists(g, 1, G, -(-T // block), 0.2)
+    out, lse = spa.spa_sparse_attn_tree(q, kc, vc, parents, block, idx, count, 0.09, want_lse=True)
+    ok()
+    one = [0, 9]                                       # two heads: the rest is the same
+    want, wl, mag, qk = ref_tree(q[:, one], kc.expand(1, 2, T, 128), vc.expand(1, 2, T, 128), parents, block,
+                                 keep[:, one], 0.09, None)
+    d = 2.0 ** -17 * qk + 2.0 ** -18
+    assert bool(((out[:, one].double() - want).abs() <= (1.02 * U + 2 * d[..., None]) * mag + U * want.abs()).all())
+    assert bool(((lse[:, one].double() - wl).abs() <= d + 4 * E * wl.abs()).all())
+
+
+def test_offsets_beyond_32_bits():
+    # caches of 2.3 G elements: rows at their far end
+    g = gen(14)
+    B, Hq, Hkv, n, T, d = 2, 8, 8, 2, 1_100_000, 128
+    kc, vc = (torch.zeros(B, Hkv, T, d, device="cuda", dtype=BF) for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    kc[1, 7].normal_(generator=g)
+    vc[1, 7].normal_(generator=g)
+    q, k, v = randn(g, B, Hq, n, d), randn(g, B, Hkv, n, d), randn(g, B, Hkv, n, d)
+    freqs, m = spa.spa_rope_frequencies(d)
+    qr = spa.spa_rope_append(q, k, v, kc, vc, freqs, m, row0=T - n)
+    pos = torch.arange(T - n, T, device="cuda").expand(B, n)
+    want, mag = ref_rope(k, pos, freqs, m, "half")
+    close_rope(kc[:, :, T - n:], want, mag, BF)
+    assert torch.equal(vc[:, :, T - n:], v)
+    parents = torch.tensor([[-1, 0]] * B, device="cuda", dtype=torch.int32)
+    out, lse = spa.spa_sparse_attn_tree(qr, kc, vc, parents, 64, None, None, 0.09, want_lse=True)
+    last = qr[:, :, 1:].contiguous()
+    w = spa.spa_attn_weight(last, kc, lse[:, :, 1:].contiguous(), 0.09)
+    keep, count = spa.spa_evict_select(w, 50, 4, 4)
+    k2, v2, _ = spa.spa_cache_gather(kc, vc, keep, count)
+    ok()
+    check_tree(qr[1:, 7:], kc[1:, 7:], vc[1:, 7:], parents[1:], 64, None, 0.09, None, out[1:, 7:], lse[1:, 7:])
+    ww, tol = ref_weight(last[1:, 7:], kc[1:, 7:], lse[1:, 7:, 1:], 0.09, 64, None, None, None, 1.0)
+    assert bool(((w[1:, 7:].double() - ww).abs() <= tol).all())
+    assert keep[1, 7, -4:].tolist() == list(range(T - 4, T))
+    assert torch.equal(k2[1, 7], kc[1, 7, keep[1, 7].long()]) and torch.equal(v2[1, 7], vc[1, 7, keep[1, 7].long()])
+
+
+def test_two_calls_at_once_on_two_streams():
+    g = gen(15)
+    args = []
+    for T in (3000, 5000):
+        q, kc, vc = randn(g, 1, 8, 20, 128), randn(g, 1, 2, T, 128), randn(g, 1, 2, T, 128)
+        args.append((q, kc, vc, tree_of(g, 1, 20), 64, None, None, 0.09))
+    want = [spa.spa_sparse_attn_tree(*a, want_lse=True) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(20):
+        got = [spa.spa_sparse_attn_tree(*a, want_lse=True, stream=st) for a, st in zip(args, streams)]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    ok()
 
 
 def test_tree_of_large_logits():
@@ -354,6 +419,12 @@ def ref_weight(q, k, lse, scale, block, keep, lens, prev, decay):
     (2, 4, 4, 2, 4097, 128, 32, None, True),
     (1, 16, 1, 200, 333, 128, 128, None, True),
     (1, 5, 1, 130, 260, 64, 128, 0.7, False),
+    (40, 4, 2, 1, 300, 64, 16, None, True),            # more sequences than lanes
+    (1, 8, 2, 1, 40001, 128, 16, 0.4, False),          # lists beyond a thousand entries
+    (1, 4, 4, 4, 50, 128, 16, 0.6, False),             # four queries over two query blocks
+    (1, 8, 2, 16, 3001, 128, 64, None, False),         # one query tile of 64 rows
+    (1, 8, 2, 1500, 2500, 128, 128, None, False),      # runs of several pairs, joined
+    (35, 8, 1, 40, 200, 64, 64, None, True),
 ])
 def test_weight_matches_fp64(B, Hq, Hkv, Lq, T, d, block, p, ragged):
     g = gen(T + Lq)
@@ -439,6 +510,7 @@ def ref_evict(score, lens, n_keep, n_sink, n_recent):
     (1, 1, 1, 1, 0, 0, False, "random"), (1, 1, 5, 9, 2, 3, False, "random"), (2, 3, 100, 10, 4, 6, False, "random"),
     (2, 2, 1000, 333, 0, 0, True, "random"), (3, 2, 1000, 999, 5, 100, True, "equal"), (1, 2, 4097, 1, 0, 0, False, "equal"),
     (1, 1, 40000, 5000, 4, 128, False, "few"), (2, 1, 20000, 19999, 1, 1, True, "random"),
+    (1, 1, 400001, 3000, 4, 32, False, "random"),       # more keys than a cluster holds
     (1, 2, 70001, 512, 0, 64, False, "wild"), (2, 1, 9000, 4000, 8, 8, False, "wild"), (4, 1, 300, 64, 64, 0, True, "few"),
 ])
 def test_evict_select_is_exact(B, Hkv, T, n_keep, n_sink, n_recent, ragged, kind):
