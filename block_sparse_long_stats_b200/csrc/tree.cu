@@ -219,6 +219,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     const int row0 = blockIdx.x % a.nrt * 128;     // this CTA's rows of every (b, kv-head)
+    // Up to 64 rows fill two of the softmax warps. The SM's second CTA (the grid's second
+    // 148) takes the other two lane quarters, whose warps issue on the SM's other two
+    // sub-partitions.
+    const int shift = a.G * a.n - row0 <= 64 && blockIdx.x >= kCtas / 2 ? 64 : 0;
     bool ok = true;                    // cleared by a wait that ran out: no more work, no waits
     tc_fence_before();
     __syncthreads();
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!sg.more) break;
         if (warp == 4 && lane == 0 && ok) {
             mbar_arrive_expect_tx(&bar_q, C::SLOT);
-            const int qrow = sg.unit * a.G * a.n + row0;
+            const int qrow = sg.unit * a.G * a.n + row0 - shift;   // rows before q: zero-filled
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf) tma_load_2d(smem + hf * C::HALF, &tq, &bar_q, hf * 64, qrow);
         }
@@ -461,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             } else {
                 // ------------------------------------ softmax
-                const int r = tid, row = row0 + r, node = row % a.n, head = row / a.n & 15;
-                const bool live = row < a.G * a.n &&
+                const int r = tid, row = row0 + max(r - shift, 0), node = row % a.n, head = row / a.n & 15;
+                const bool live = r >= shift && row < a.G * a.n &&
                                   (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) != 0u;
                 const bool warp_live = __any_sync(0xffffffffu, live);
                 const uint32_t t_s = tmem_slot + ((uint32_t)(warp * 32) << 16), t_o = t_s + 128;
@@ -626,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
         // ------------------------------------------------ the segment's state
         if (warp < 4) {
-            const int r = tid, row = row0 + r, node = row % a.n;
+            const int r = tid - shift, row = row0 + max(r, 0), node = row % a.n;
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_done, sg.segs & 1, a.err));
             tc_fence_after();
-            const bool store = row < a.G * a.n, whole = sg.whole;
+            const bool store = r >= 0 && row < a.G * a.n, whole = sg.whole;
             if (!store || (nmask[node][0] | nmask[node][1] | nmask[node][2] | nmask[node][3]) == 0u) {
                 m_used = -INFINITY;                      // an unused row: no key
                 l = 0.f;
