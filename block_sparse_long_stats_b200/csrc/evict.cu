@@ -139,14 +139,23 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             *reinterpret_cast<int4 *>(own + 4) = *reinterpret_cast<const int4 *>(hs + 8 * lane + 4);
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] = own[e];
+            // (in fours: every load of a group on its way before the first is used)
+            for (int r0 = 1; r0 < C; r0 += 4) {
+                int4 x[4], y[4];
 #pragma unroll
-            for (int r = 1; r < kMaxCluster; ++r)
-                if (r < C) {
-                    const int4 *o = reinterpret_cast<const int4 *>(cl.map_shared_rank(hs, (rank + r) % C) + 8 * lane);
-                    const int4 x = o[0], y = o[1];
-                    sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
-                    sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
+                for (int j = 0; j < 4; ++j) {
+                    const int4 *o = reinterpret_cast<const int4 *>(
+                        cl.map_shared_rank(hs, r0 + j < C ? (rank + r0 + j) % C : rank) + 8 * lane);
+                    x[j] = o[0];
+                    y[j] = o[1];
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r0 + j < C) {
+                        sum[0] += x[j].x; sum[1] += x[j].y; sum[2] += x[j].z; sum[3] += x[j].w;
+                        sum[4] += y[j].x; sum[5] += y[j].y; sum[6] += y[j].z; sum[7] += y[j].w;
+                    }
+            }
             int mine_all = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) mine_all += sum[e];
