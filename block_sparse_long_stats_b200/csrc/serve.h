@@ -11,7 +11,8 @@ namespace spa {
 
 // Programmatic dependent launch: a kernel launched by launch_early may start while the
 // one before it on the stream still runs (its launch and set-up are hidden), and calls
-// grid_wait before it touches global memory: from there on everything before it is done.
+// grid_wait before it touches global memory or takes tensor memory: from there on
+// everything before it is done.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 inline cudaError_t launch_early(const void *kern, dim3 grid, dim3 block, size_t smem, void **args, cudaStream_t s,

@@ -22,10 +22,18 @@
 //   warps 0-3 : softmax; thread r owns row r = TMEM lane r
 //   warp 4    : TMA producer (Q per unit; K and V tiles)
 //   warp 5    : TMEM allocator and tcgen05.mma issuer
-// Tried: one CTA per SM with two softmax warpgroups and deeper rings (33 nodes on eight
-// ragged caches 107 us against XX, one or two MMA warps), and halves of 64 keys with a score
-// tile each, so that a warpgroup's softmax overlaps its own products (134 us: a step with
-// N = 64 takes nearly as long as one with N = 128).
+//
+// Measured (B200, main kernel): 16 nodes, 32/8 heads over four 128K caches, half of the
+// 16-key blocks kept: 196-200 us, 5.4 TB/s of kept K and V (and slower under the power cap:
+// half of the products' rows are empty). 64 nodes over 32K: 47-49 us; 33 nodes, 40/8 heads
+// over eight ragged caches of up to 16000 keys: 102-108 us; there a tile takes 4600 cycles
+// with two CTAs on the SM: 2500 of softmax, 2000 for the products, which wait for one another.
+// Tried: blocks side by side copied in boxes of up to 128 rows (210 us for the first case:
+// the longer issuing loop costs more than the fewer boxes save), one CTA per SM with two
+// softmax warpgroups and deeper rings (107 us for the last case with one MMA warp, 117 with
+// two), and halves of 64 keys with a score tile each, so that a warpgroup's softmax
+// overlaps its own products (134 us: a step with N = 64 takes nearly as long as one with
+// N = 128).
 #include <math.h>
 
 #include "serve.h"
@@ -207,8 +215,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
     }
-    if (warp == 5) tmem_alloc(&tmem_slot, 256);
+    // tensor memory only after the wait: taken earlier it could be what a kernel that this one
+    // waits for is waiting for
     grid_wait();
+    if (warp == 5) tmem_alloc(&tmem_slot, 256);
     if (warp == 0) {
         const int total = run_total(a), chunk = run_chunk(a, total);
         if (lane == 0) {

@@ -258,13 +258,15 @@ def test_tree_matches_fp64(B, Hq, Hkv, n, T, d, block, p, ragged):
     assert torch.equal(again, out)
 
 
-def test_tree_lists_longer_than_a_stretch():
-    # 2048 rows leave few runs: each walks over several stretches of its long lists
+@pytest.mark.parametrize("p,block", [(0.2, 16), (0.95, 16), (0.8, 32)])
+def test_tree_lists_longer_than_a_stretch(p, block):
+    # 2048 rows leave few runs: each walks over several stretches of its long lists, with
+    # blocks alone or side by side
     g = gen(13)
-    G, n, T, block = 16, 128, 450000, 16
+    G, n, T = 16, 128, 450000
     q, kc, vc = randn(g, 1, G, n, 128), randn(g, 1, 1, T, 128), randn(g, 1, 1, T, 128)
     parents = tree_of(g, 1, n)
-    idx, count, keep = lists(g, 1, G, -(-T // block), 0.2)
+    idx, count, keep = lists(g, 1, G, -(-T // block), p)
     out, lse = spa.spa_sparse_attn_tree(q, kc, vc, parents, block, idx, count, 0.09, want_lse=True)
     ok()
     one = [0, 9]                                       # two heads: the rest is the same
@@ -563,6 +565,9 @@ def test_cache_gather_moves_rows_and_leaves_the_rest(dtype, d):
             t = keep[b, h, :c].long()
             wk[b, h, :c], wv[b, h, :c], ws[b, h, :c] = kc[b, h, t], vc[b, h, t], score[b, h, t]
     assert torch.equal(ko, wk) and torch.equal(vo, wv) and torch.equal(so, ws)
+    k1, v1, s1 = spa.spa_cache_gather(kc, vc, keep)                 # every entry of the list
+    at = keep.long()[..., None].expand(-1, -1, -1, d)
+    assert s1 is None and torch.equal(k1, kc.gather(2, at)) and torch.equal(v1, vc.gather(2, at))
     keep[0, 1, 3], keep[0, 0, 5] = -1, T
     spa.spa_cache_gather(kc, vc, keep, torch.tensor([37, 38, -1], device="cuda", dtype=torch.int32), k_out=ko, v_out=vo)
     torch.cuda.synchronize()
