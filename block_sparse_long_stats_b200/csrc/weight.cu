@@ -25,7 +25,7 @@
 // warp 17: TMEM allocator and tcgen05.mma issuer.
 //
 // Measured (B200): a decode step's weight over four 128K caches with three quarters of the
-// blocks kept 151 us (5.5 TB/s, 84 % of the measured copy bandwidth; weight_few_kernel),
+// blocks kept 142 us (5.9 TB/s, 90 % of the measured copy bandwidth; weight_few_kernel),
 // 128 queries over 32K keys 59 us, all queries of a 4K prompt 106 us; in the last two ex2
 // is busy half of the time, and the sums of a pair take 3400 cycles where 2.2 of a
 // sub-partition's four warps are at them at a time.
@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // on their way meanwhile. A quad holds a key's row and adds its weights. Equal runs of 16-key
 // slabs over all warps.
 constexpr int kSlab = 16;
-constexpr int kFar = 4;                      // slabs ahead that are brought into L2
+constexpr int kFar = 1;                      // slabs behind the next one that are brought into L2
+                                             // (decode step below: none 161 us, 1 142, 2 143, 4 152, 8 193)
 constexpr int kFewThreads = 256, kFewCtas = 2 * kCtas;
 
 template <int D, int NT>

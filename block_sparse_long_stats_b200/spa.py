@@ -653,19 +653,23 @@ def spa_rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, mscal
 
     def call(st):
         nonlocal q_out, k_out
+        qp, qs = _strided(q, "q", q.shape, dt, dev)
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        qp, qs = _strided(q, "q", q.shape, dt, dev)
-        qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
+            qop, qos = q_out.data_ptr(), None
+        else:
+            qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp = ks = kop = kos = None
         Hkv = 0
         if k is not None:
             Hkv = k.shape[1]
             shape = (B, Hkv, L, d)
+            kp, ks = _strided(k, "k", shape, dt, dev)
             if k_out is None:
                 k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            kp, ks = _strided(k, "k", shape, dt, dev)
-            kop, kos = _strided(k_out, "k_out", shape, dt, dev)
+                kop, kos = k_out.data_ptr(), None
+            else:
+                kop, kos = _strided(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
             raise ValueError("k_out without k")
         _check("spa_rope",
@@ -690,10 +694,12 @@ def spa_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kc: torch
 
     def call(st):
         nonlocal q_out
+        qp, qs = _strided(q, "q", q.shape, dt, dev)
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        qp, qs = _strided(q, "q", q.shape, dt, dev)
-        qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
+            qop, qos = q_out.data_ptr(), None
+        else:
+            qop, qos = _strided(q_out, "q_out", q.shape, dt, dev)
         kp, ks = _strided(k, "k", (B, Hkv, L, d), dt, dev)
         vp, vs = _strided(v, "v", (B, Hkv, L, d), dt, dev)
         _check("spa_rope_append",
@@ -748,8 +754,14 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            op = out.data_ptr()
+        else:
+            op = _arg(out, "out", q.shape, dt, dev)
         if lse is None and want_lse:
             lse = q.new_empty((B, Hq, n), dtype=torch.float32)
+            lp = lse.data_ptr()
+        else:
+            lp = _arg(lse, "lse", (B, Hq, n), torch.float32, dev)
         ip, cap, cp = _lists(idx, count, B, Hq, 1, dev)
         _check("spa_sparse_attn_tree",
                lib().spa_sparse_attn_tree(_arg(q, "q", q.shape, dt, dev),
@@ -759,8 +771,7 @@ def spa_sparse_attn_tree(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor,
                                           _arg(lens, "lens", (B,), torch.int32, dev), ip, cap, cp,
                                           scale, workspace.data_ptr(),
                                           workspace.numel() * workspace.element_size(),
-                                          _arg(out, "out", q.shape, dt, dev),
-                                          _arg(lse, "lse", (B, Hq, n), torch.float32, dev), st))
+                                          op, lp, st))
         return out, lse
 
     return _enqueue(call, q, stream)
@@ -796,6 +807,9 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         if out is None:
             out = q.new_empty((B, Hkv, T), dtype=torch.float32)
+            op = out.data_ptr()
+        else:
+            op = _arg(out, "out", (B, Hkv, T), torch.float32, dev)
         _check("spa_attn_weight",
                lib().spa_attn_weight(_arg(q, "q", q.shape, dt, dev), _arg(k, "k", (B, Hkv, T, d), dt, dev),
                                      _dt(q), B, Hq, Hkv, Lq, T, d,
@@ -803,7 +817,7 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
                                      _arg(lens, "lens", (B,), torch.int32, dev), block, ip, cap, cp, scale,
                                      _arg(prev, "prev", (B, Hkv, T), torch.float32, dev), decay,
                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                     _arg(out, "out", (B, Hkv, T), torch.float32, dev), st))
+                                     op, st))
         return out
 
     return _enqueue(call, q, stream)
