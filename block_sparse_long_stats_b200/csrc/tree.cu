@@ -28,8 +28,8 @@
 // half of the products' rows are empty). 64 nodes over 32K: 47-49 us; 33 nodes, 40/8 heads
 // over eight ragged caches of up to 16000 keys: 102-108 us; there a tile takes 4600 cycles
 // with two CTAs on the SM: 2500 of softmax, 2000 for the products, which wait for one another.
-// Tried: blocks side by side copied in boxes of up to 128 rows (210 us for the first case:
-// the longer issuing loop costs more than the fewer boxes save), one CTA per SM with two
+// Tried: runs of two and four blocks copied in boxes of their own too (210 us for the first
+// case: the longer issuing loop costs more than the fewer boxes save), one CTA per SM with two
 // softmax warpgroups and deeper rings (107 us for the last case with one MMA warp, 117 with
 // two), and halves of 64 keys with a score tile each, so that a warpgroup's softmax
 // overlaps its own products (134 us: a step with N = 64 takes nearly as long as one with
@@ -180,7 +180,8 @@ struct Segment {
 template <int D, int BLK>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
+                const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tk1,
+                const __grid_constant__ CUtensorMap tv1, const __grid_constant__ TreeArgs a) {
     using C = Cfg<D, BLK>;
     constexpr int PER = C::PER, ST = C::ST;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -415,6 +416,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                             uint32_t hm;
                             rw[e] = kv_row0 + (tree ? sg.P + e * BLK : block_at(min(u * PER + e, nu - 1), hm) * BLK);
                         }
+                        // (lists ascend) a tile of blocks that follow one another: one box. With every
+                        // 16-key block of four 128K caches kept 344 us against 357, 6.2 TB/s.
+                        const bool side_by_side = nblk == PER && rw[PER - 1] - rw[0] == (PER - 1) * BLK;
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv) {
                             uint64_t *full = kv ? &full_v[s] : &full_k[s];
@@ -424,6 +428,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                             }
                             mbar_arrive_expect_tx(full, (uint32_t)(nblk * BLK * D * 2));
                             unsigned char *dst = smem + (kv ? C::OFF_V : C::OFF_K) + s * C::SLOT;
+                            if (PER > 1 && side_by_side) {
+#pragma unroll
+                                for (int hf = 0; hf < C::HALVES; ++hf)
+                                    tma_load_2d(dst + hf * C::HALF, kv ? &tv1 : &tk1, full, hf * 64, rw[0]);
+                                continue;
+                            }
 #pragma unroll
                             for (int e = 0; e < PER; ++e)
                                 if (e < nblk) {
@@ -779,17 +789,19 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t rows, int d, int box_
 template <int D, int BLK>
 cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
     using C = Cfg<D, BLK>;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mk1, mv1;             // mk1, mv1: boxes of a whole tile
     const uint64_t kv_rows = (uint64_t)c.B * c.Hkv * c.T;
     if (!make_map(&mq, c.q, (uint64_t)c.B * c.Hq * c.n, D, 128) || !make_map(&mk, c.kc, kv_rows, D, BLK) ||
         !make_map(&mv, c.vc, kv_rows, D, BLK))
+        return cudaErrorNotSupported;
+    if (C::PER > 1 && (!make_map(&mk1, c.kc, kv_rows, D, kTile) || !make_map(&mv1, c.vc, kv_rows, D, kTile)))
         return cudaErrorNotSupported;
     cudaError_t e = allow_smem<tree_kernel<D, BLK>>(C::SMEM);
     if (e != cudaSuccess) return e;
     // no more CTAs than runs of kMinTiles tiles (the most that the lengths allow)
     const long long most = (long long)c.B * c.Hkv * ((c.T - c.n + kTile - 1) / kTile + 1);
     const long long runs = (most + kMinTiles - 1) / kMinTiles;
-    void *args[] = {&mq, &mk, &mv, &a};
+    void *args[] = {&mq, &mk, &mv, &mk1, &mv1, &a};
     e = launch_early(reinterpret_cast<const void *>(tree_kernel<D, BLK>),
                      dim3((unsigned)((runs < a.runs ? runs : a.runs) * a.nrt)), dim3(kThreads), C::SMEM, args, s);
     if (e != cudaSuccess) return e;

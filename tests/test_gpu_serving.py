@@ -380,6 +380,33 @@ def test_tree_of_one_node_is_decode():
     ok()
 
 
+def test_wrong_shapes_types_and_strides_are_refused():
+    g = gen(16)
+    q, kc, vc = randn(g, 1, 4, 3, 128), randn(g, 1, 2, 50, 128), randn(g, 1, 2, 50, 128)
+    parents = torch.full((1, 3), -1, device="cuda", dtype=torch.int32)
+    idx, count = torch.zeros(1, 4, 1, 4, device="cuda", dtype=torch.int32), torch.zeros(1, 4, 1, device="cuda", dtype=torch.int32)
+    call = spa.spa_sparse_attn_tree
+    for args in ((q, kc, vc[:, :1], parents, 16, None, None, 0.1), (q, kc, vc, parents.long(), 16, None, None, 0.1),
+                 (q, kc, vc, parents[:, :2], 16, None, None, 0.1), (q.float(), kc, vc, parents, 16, None, None, 0.1),
+                 (q, kc.transpose(1, 2).contiguous().transpose(1, 2), vc, parents, 16, None, None, 0.1),
+                 (q, kc, vc, parents, 16, idx, None, 0.1), (q, kc, vc, parents, 16, idx, count[:, :2], 0.1)):
+        with pytest.raises(ValueError):
+            call(*args)
+    with pytest.raises(spa.SpaError):
+        call(q, kc, vc, parents, 16, None, None, 0.1, workspace=torch.empty(64, device="cuda", dtype=torch.uint8))
+    freqs, _ = spa.spa_rope_frequencies(128)
+    for bad in (freqs.float(), freqs.cuda(), freqs.reshape(2, 32)):
+        with pytest.raises(ValueError):
+            spa.spa_rope(q, None, bad)
+    with pytest.raises(ValueError):
+        spa.spa_rope(q.transpose(2, 3), None, freqs)                # features not contiguous
+    with pytest.raises(ValueError):
+        spa.spa_attn_weight(q, kc, torch.zeros(1, 4, 2, device="cuda"), 0.1)
+    with pytest.raises(ValueError):
+        spa.spa_cache_gather(kc, vc, idx.reshape(1, 4, 4))
+    ok()
+
+
 # ---------------------------------------------------------------- accumulated weight
 
 def ref_weight(q, k, lse, scale, block, keep, lens, prev, decay):
