@@ -41,7 +41,7 @@ constexpr int kGroups = 4;             // consumer warpgroups
 constexpr int kConsumers = kGroups * 128;
 constexpr int kThreads = kConsumers + 96;
 constexpr int kTile = 128;             // keys
-constexpr int kUnits = 8;              // key tiles that warpgroups may be apart by, and more
+constexpr int kUnits = 8;              // key tiles whose sums may be open at once: below 7 (two score tiles)
 constexpr int kMarkChunk = 512;        // blocks per CTA of the mark kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -404,150 +404,168 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!col || x.qi * a.pc + ci >= a.Lq) return -INFINITY;
             return __ldg(a.lse + ((size_t)x.bg * a.G + ch) * a.Lq + x.qi * a.pc + ci);
         };
-        Pair pn = p;                           // this group's next pair
-        float nl_next = 0.f;
-        if (a.nqt > 1 && buf < jobs) {
-            for (int i = 0; i < buf; ++i) {
-                bool head;
-                pn.next(a, head);
+        // The key tile's sum over the groups: each brings its own once (zero where it had no
+        // pair), and of the four warps with the same keys the last one adds them up, in the
+        // groups' order. No group waits for another; the score tiles keep them within a few jobs.
+        auto bring = [&](const Pair &x, int unit, bool whole, bool first, float value) {
+            const int slot = unit % kUnits, rows32 = warp & 3;
+            red[slot][wg][r] = value;
+            __threadfence_block();
+            __syncwarp();
+            int before = 0;
+            if (lane == 0) before = atomicAdd(&arrived[slot][rows32], 1);
+            if (__shfl_sync(0xffffffffu, before, 0) != kGroups - 1) return;
+            __threadfence_block();
+            if (lane == 0) arrived[slot][rows32] = 0;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w) s += *reinterpret_cast<volatile float *>(&red[slot][w][r]);
+            const int t = x.kt * kTile + r;
+            if (t >= x.off + a.Lq) s = 0.f;
+            if (t >= a.T) return;
+            if (whole) {
+                const size_t o = (size_t)x.bg * a.T + t;
+                a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
+            } else {
+                a.parts[((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kTile + r] = s;
             }
-            nl_next = column(pn);
-        }
-        bool ok = true, fresh = true;          // fresh: this group's columns changed
-        float sum = 0.f;
-        int units = 0;
-        int unit_first = 0;                    // the key tile's first pair in this run
-        const int first_qi = jobs > 0 ? first_tile(a, p.kt, p.off) : 0;
-        bool from_start = jobs > 0 && p.qi == first_qi;
-        for (int m = 0; m < jobs; ++m) {
-            const bool mine = m % BUFS == buf;
-            const int t = p.kt * kTile + r;
-            const size_t o = (size_t)p.bg * a.T + t;
-            const bool last_pair = p.qi == a.nqt - 1;      // of the key tile
-            if (mine) {
-                // loads that need no score: ahead of the wait (the columns' lse a job ahead)
-                const float nl = nl_next;
-                if (a.nqt > 1 && m + BUFS < jobs) {
-#pragma unroll
-                    for (int i = 0; i < BUFS; ++i) {
-                        bool head;
-                        pn.next(a, head);
-                    }
-                    nl_next = column(pn);
+        };
+        // this group walks over the run by its own pairs: p is pair m; a key tile that ends (or
+        // is cut by the run's end) on the way is handed to `ended`
+        int m = 0, units = 0, unit_first = 0;
+        bool from_start = jobs > 0 && p.qi == first_tile(a, p.kt, p.off);
+        auto advance = [&](int steps, auto &&ended) -> bool {
+            for (;;) {
+                const int rest = a.nqt - p.qi, left = jobs - m;      // pairs of the key tile, of the run
+                if (steps < min(rest, left)) {
+                    p.qi += steps;
+                    m += steps;
+                    return true;
                 }
-                float before = 0.f;
-                if (!STREAM && a.prev && t < a.T) before = a.prev[o];
-                uint32_t see[4];
-                bool masked = false;
-                const int q0 = p.off + p.qi * a.pc;        // position of the tile's first query
-                const int lim = t - q0;                    // positions from lim on see the key
-                if (a.marks) {
-                    masked = true;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) see[c] = 0u;
-                    const int blk = t / a.block, qb0 = p.off / a.block;
-                    if (t < a.T) {
-                        const uint16_t *mk = a.marks + (size_t)p.bg * a.nq * a.nbp + blk;
-                        {
-                            const int q_end = min(a.Lq, (p.qi + 1) * a.pc) + p.off;
-                            for (int qb = q0 / a.block; qb * a.block < q_end; ++qb) {
-                                const uint32_t hm = mk[(size_t)(qb - qb0) * a.nbp];
-                                const int lo = max(max(qb * a.block - q0, 0), lim);
-                                const int hi = min((qb + 1) * a.block, q_end) - q0;
-                                if (lo < hi)
-                                    for (int h = 0; h < a.G; ++h)
-                                        if ((hm >> h) & 1u) set_range(see, h * a.pc + lo - col0, h * a.pc + hi - col0);
-                            }
-                        }
-                    }
-                } else if (p.kt * kTile + kTile - 1 > q0) {        // the causal border
-                    masked = true;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) see[c] = 0u;
-                    if (lim < a.pc)
-                        for (int h = 0; h < a.G; ++h) set_range(see, h * a.pc + max(lim, 0) - col0, (h + 1) * a.pc - col0);
-                }
-                if (fresh) {
-                    named_bar_sync(2 + wg, 128);           // the group is done with the last columns
-                    if (r < COLS) nl_s[wg][r] = minus_log2(a.nqt > 1 ? nl : column(p));
-                    named_bar_sync(2 + wg, 128);
-                }
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (uint32_t)((m / BUFS) & 1), a.err));
-                if (ok) {
-                    tc_fence_after();
-                    uint64_t acc[2] = {0ull, 0ull};
-                    const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
-                    float x[2][16];
-                    tmem_ld16f(t_s, x[0]);
-#pragma unroll
-                    for (int c0 = 0; c0 < COLS; c0 += 16) {
-                        tc_wait_ld();
-                        float *y = x[(c0 / 16) & 1];
-                        if (c0 + 16 < COLS) tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
-                        // a key no one keeps may hold anything: select (few tiles have a mask:
-                        // __any_sync keeps this a branch; as selects it took as long as the sums)
-                        if (__any_sync(0xffffffffu, masked)) {
-                            const uint32_t bits = see[c0 >> 5] >> (c0 & 16);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 n4 = *reinterpret_cast<const float4 *>(&nl_s[wg][c0 + e]);
-                            float y0, y1, y2, y3;
-                            f32x2_split(fma_f32x2(f32x2(y[e], y[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
-                            f32x2_split(fma_f32x2(f32x2(y[e + 2], y[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
-                            acc[0] = add_f32x2(acc[0], f32x2(fast_exp2(y0), fast_exp2(y1)));
-                            acc[1] = add_f32x2(acc[1], f32x2(fast_exp2(y2), fast_exp2(y3)));
-                        }
-                    }
-                    float s0, s1;
-                    f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
-                    sum += s0 + s1;
-                    tc_fence_before();
-                    mbar_arrive(&s_empty[buf]);
-                }
-                fresh = false;
-                if (!STREAM) {                              // the key tile's only pair
-                    if (t < a.T) {
-                        const bool in = t < p.off + a.Lq;
-                        a.out[o] = a.prev ? fmaf(a.decay, before, in ? sum : 0.f) : (in ? sum : 0.f);
-                    }
-                    sum = 0.f;
-                }
-            }
-            if (STREAM && (last_pair || m + 1 == jobs)) {
-                // The key tile's sum over the groups: each brings its own, and of the four warps
-                // with the same keys the last one adds them up, in the groups' order. No group
-                // waits for another; the score tiles keep them within four jobs.
-                const int slot = units % kUnits, rows32 = warp & 3;
-                red[slot][wg][r] = sum;
-                sum = 0.f;
-                __threadfence_block();
-                __syncwarp();
-                int before = 0;
-                if (lane == 0) before = atomicAdd(&arrived[slot][rows32], 1);
-                if (__shfl_sync(0xffffffffu, before, 0) == kGroups - 1) {
-                    __threadfence_block();
-                    if (lane == 0) arrived[slot][rows32] = 0;
-                    float s = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kGroups; ++w) s += *reinterpret_cast<volatile float *>(&red[slot][w][r]);
-                    if (t >= p.off + a.Lq) s = 0.f;
-                    if (t < a.T) {
-                        if (from_start && last_pair)
-                            a.out[o] = a.prev ? fmaf(a.decay, a.prev[o], s) : s;
-                        else
-                            a.parts[((size_t)blockIdx.x * 2 + (unit_first > 0 ? 1 : 0)) * kTile + r] = s;
-                    }
-                }
+                ended(from_start && rest <= left, unit_first == 0);
+                if (rest >= left) return false;
+                m += rest;
+                steps -= rest;
                 ++units;
-                unit_first = m + 1;
+                unit_first = m;
                 from_start = true;
+                p.qi = a.nqt - 1;
+                bool head;
+                p.next(a, head);
             }
-            bool head;
-            p.next(a, head);
-            fresh = fresh || head || a.nqt > 1;
+        };
+        bool ok = true, more = jobs > 0;
+        if (more)
+            more = advance(buf, [&](bool whole, bool first) {
+                if (STREAM) bring(p, units, whole, first, 0.f);
+            });
+        float sum = 0.f, nl_next = more && a.nqt > 1 ? column(p) : 0.f;
+        int bg_cols = -1;                      // whose columns nl_s holds (one query tile per head)
+        while (more) {
+            // this pair, and where the next one lies (the columns' lse a pair ahead)
+            const Pair at = p;
+            const int mc = m;
+            const float nl = nl_next;
+            const bool fresh = a.nqt > 1 || at.bg != bg_cols;
+            bg_cols = at.bg;
+            int unit = -1;
+            bool unit_whole = false, unit_begins = false;
+            more = advance(BUFS, [&](bool whole, bool first) {
+                if (!STREAM) return;
+                if (unit < 0) {            // this pair's key tile: once its sum is there
+                    unit = units;
+                    unit_whole = whole;
+                    unit_begins = first;
+                } else {
+                    bring(p, units, whole, first, 0.f);
+                }
+            });
+            if (more && a.nqt > 1) nl_next = column(p);
+            const int t = at.kt * kTile + r;
+            const size_t o = (size_t)at.bg * a.T + t;
+            float before = 0.f;
+            if (!STREAM && a.prev && t < a.T) before = a.prev[o];
+            uint32_t see[4];
+            bool masked = false;
+            const int q0 = at.off + at.qi * a.pc;        // position of the tile's first query
+            const int lim = t - q0;                    // positions from lim on see the key
+            if (a.marks) {
+                masked = true;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) see[c] = 0u;
+                const int blk = t / a.block, qb0 = at.off / a.block;
+                if (t < a.T) {
+                    const uint16_t *mk = a.marks + (size_t)at.bg * a.nq * a.nbp + blk;
+                    {
+                        const int q_end = min(a.Lq, (at.qi + 1) * a.pc) + at.off;
+                        for (int qb = q0 / a.block; qb * a.block < q_end; ++qb) {
+                            const uint32_t hm = mk[(size_t)(qb - qb0) * a.nbp];
+                            const int lo = max(max(qb * a.block - q0, 0), lim);
+                            const int hi = min((qb + 1) * a.block, q_end) - q0;
+                            if (lo < hi)
+                                for (int h = 0; h < a.G; ++h)
+                                    if ((hm >> h) & 1u) set_range(see, h * a.pc + lo - col0, h * a.pc + hi - col0);
+                        }
+                    }
+                }
+            } else if (at.kt * kTile + kTile - 1 > q0) {        // the causal border
+                masked = true;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) see[c] = 0u;
+                if (lim < a.pc)
+                    for (int h = 0; h < a.G; ++h) set_range(see, h * a.pc + max(lim, 0) - col0, (h + 1) * a.pc - col0);
+            }
+            if (fresh) {
+                named_bar_sync(2 + wg, 128);           // the group is done with the last columns
+                if (r < COLS) nl_s[wg][r] = minus_log2(a.nqt > 1 ? nl : column(at));
+                named_bar_sync(2 + wg, 128);
+            }
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (uint32_t)((mc / BUFS) & 1), a.err));
+            if (ok) {
+                tc_fence_after();
+                uint64_t acc[2] = {0ull, 0ull};
+                const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+                float x[2][16];
+                tmem_ld16f(t_s, x[0]);
+#pragma unroll
+                for (int c0 = 0; c0 < COLS; c0 += 16) {
+                    tc_wait_ld();
+                    float *y = x[(c0 / 16) & 1];
+                    if (c0 + 16 < COLS) tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
+                    // a key no one keeps may hold anything: select (few tiles have a mask:
+                    // __any_sync keeps this a branch; as selects it took as long as the sums)
+                    if (__any_sync(0xffffffffu, masked)) {
+                        const uint32_t bits = see[c0 >> 5] >> (c0 & 16);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 n4 = *reinterpret_cast<const float4 *>(&nl_s[wg][c0 + e]);
+                        float y0, y1, y2, y3;
+                        f32x2_split(fma_f32x2(f32x2(y[e], y[e + 1]), scale2, f32x2(n4.x, n4.y)), y0, y1);
+                        f32x2_split(fma_f32x2(f32x2(y[e + 2], y[e + 3]), scale2, f32x2(n4.z, n4.w)), y2, y3);
+                        acc[0] = add_f32x2(acc[0], f32x2(fast_exp2(y0), fast_exp2(y1)));
+                        acc[1] = add_f32x2(acc[1], f32x2(fast_exp2(y2), fast_exp2(y3)));
+                    }
+                }
+                float s0, s1;
+                f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
+                sum += s0 + s1;
+                tc_fence_before();
+                mbar_arrive(&s_empty[buf]);
+            }
+            if (!STREAM) {                              // the key tile's only pair
+                if (t < a.T) {
+                    const bool in = t < at.off + a.Lq;
+                    a.out[o] = a.prev ? fmaf(a.decay, before, in ? sum : 0.f) : (in ? sum : 0.f);
+                }
+                sum = 0.f;
+            }
+            if (STREAM && unit >= 0) {
+                bring(at, unit, unit_whole, unit_begins, sum);
+                sum = 0.f;
+            }
         }
     }
     tc_fence_before();
