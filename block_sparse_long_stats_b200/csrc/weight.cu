@@ -531,7 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = 0; c0 < COLS; c0 += 16) {
                     tc_wait_ld();
                     float *y = x[(c0 / 16) & 1];
-                    if (c0 + 16 < COLS) tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
+                    if (c0 + 16 < COLS) {
+                        tmem_ld16f(t_s + c0 + 16, x[(c0 / 16 + 1) & 1]);
+                    } else {                       // all read: the next product may begin
+                        tc_fence_before();
+                        mbar_arrive(&s_empty[buf]);
+                    }
                     // a key no one keeps may hold anything: select (few tiles have a mask:
                     // __any_sync keeps this a branch; as selects it took as long as the sums)
                     if (__any_sync(0xffffffffu, masked)) {
@@ -552,8 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s0, s1;
                 f32x2_split(add_f32x2(acc[0], acc[1]), s0, s1);
                 sum += s0 + s1;
-                tc_fence_before();
-                mbar_arrive(&s_empty[buf]);
             }
             if (!STREAM) {                              // the key tile's only pair
                 if (t < a.T) {
