@@ -26,9 +26,11 @@
 //
 // Measured (B200): a decode step's weight over four 128K caches with three quarters of the
 // blocks kept 142 us (5.9 TB/s, 90 % of the measured copy bandwidth; weight_few_kernel),
-// 128 queries over 32K keys 59 us, all queries of a 4K prompt 106 us; in the last two ex2
-// is busy half of the time, and the sums of a pair take 3400 cycles where 2.2 of a
-// sub-partition's four warps are at them at a time.
+// 128 queries over 32K keys 53 us, all queries of a 4K prompt 98 us; in the last two ex2
+// is busy 57 % of the time and a scheduler issues 38 %: what is left is the latency of the
+// sums. Tried: a product of N = 128 for each warpgroup of a score tile, begun as soon as its own
+// half is read (59 us for the window: the products take longer than what the early start
+// gains), the columns' lse in two buffers with one barrier instead of two (53.4 and 99).
 #include <math.h>
 
 #include "serve.h"
