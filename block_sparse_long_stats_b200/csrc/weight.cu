@@ -30,7 +30,10 @@
 // is busy 57 % of the time and a scheduler issues 38 %: what is left is the latency of the
 // sums. Tried: a product of N = 128 for each warpgroup of a score tile, begun as soon as its own
 // half is read (59 us for the window: the products take longer than what the early start
-// gains), the columns' lse in two buffers with one barrier instead of two (53.4 and 99).
+// gains), the columns' lse in two buffers with one barrier instead of two (53.4 and 99), all four
+// warpgroups on one score tile, 64 columns each, the other tile multiplied meanwhile (61 and
+// 113; with a warp of its own for the lse 56 and 101), a quarter of the exponentials as
+// polynomials on the FMA pipes (with the last 55 and 102: ex2 is not what bounds it).
 #include <math.h>
 
 #include "serve.h"
