@@ -46,7 +46,8 @@ constexpr int kGroups = 4;             // consumer warpgroups
 constexpr int kConsumers = kGroups * 128;
 constexpr int kThreads = kConsumers + 96;
 constexpr int kTile = 128;             // keys
-constexpr int kUnits = 8;              // key tiles whose sums may be open at once: below 7 (two score tiles)
+constexpr int kUnits = 8;              // key tiles whose sums may be open at once: 7 at most (with
+                                       // two score tiles no warpgroup is more than 6 pairs ahead)
 constexpr int kMarkChunk = 512;        // blocks per CTA of the mark kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
