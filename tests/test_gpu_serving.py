@@ -486,6 +486,16 @@ def test_weight_matches_fp64(B, Hq, Hkv, Lq, T, d, block, p, ragged):
     assert torch.equal(into, got)                       # in place, and the same bits again
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,T,d,block,p,ragged", [
+    (1, 4, 2, 100, 102301, 128, 128, None, False),     # ten key tiles per CTA, of one pair each
+    (2, 8, 2, 300, 20003, 128, 64, None, True),        # five query tiles, some twenty pairs per CTA
+    (2, 8, 2, 300, 6001, 64, 128, 0.5, False),
+    (1, 8, 2, 16, 100001, 64, 32, None, False),        # a tile of 64 rows, ten key tiles per CTA
+])
+def test_weight_of_long_runs_matches_fp64(B, Hq, Hkv, Lq, T, d, block, p, ragged):
+    test_weight_matches_fp64(B, Hq, Hkv, Lq, T, d, block, p, ragged)
+
+
 def test_weight_lists_and_lengths_out_of_range_are_recorded():
     g = gen(11)
     q, k = randn(g, 1, 2, 1, 128), randn(g, 1, 1, 300, 128)
