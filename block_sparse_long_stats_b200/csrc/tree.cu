@@ -658,8 +658,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 m_used = -INFINITY;                      // an unused row: no key
                 l = 0.f;
             }
-            const bool use = ok && sg.had > 0 && l > 0.f;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            // no key: l = 0, and O may never have been written. A NaN sum is not that: it goes out
+            const bool use = ok && sg.had > 0 && l != 0.f;
+            const float inv = use ? 1.f / l : 0.f;
             const uint32_t t_o = tmem_slot + 128 + ((uint32_t)(warp * 32) << 16);
             const size_t orow = (size_t)sg.unit * a.G * a.n + row;
             // the state of this run and unit, this row tile: [D][128], a warp's rows side by side
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             if (store) {
                 if (whole) {
-                    if (a.lse) a.lse[orow] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+                    if (a.lse) a.lse[orow] = use ? (m_used + log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     reinterpret_cast<float2 *>(a.ws_ml)[slot * 128 + r] = make_float2(m_used, l);
                 }
@@ -746,12 +747,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
         float v[4][kJoinCols];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const bool in = s0 + k < ns;
+            const bool in = s0 + k < ns;                 // no run there: an empty state
             const size_t at = in ? (s0 + k) * step : 0;
             st[k] = ml[at * 128];
-            if (!in) st[k].x = -INFINITY;
 #pragma unroll
             for (int e = 0; e < kJoinCols; ++e) v[k][e] = src[(at * D + e) * 128];
+            if (in) continue;
+            st[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kJoinCols; ++e) v[k][e] = 0.f;
         }
         const float mn = fmaxf(fmaxf(M, fmaxf(st[0].x, st[1].x)), fmaxf(st[2].x, st[3].x));
         const float mb = mn == -INFINITY ? 0.f : mn, f = fast_exp2(M - mb);
@@ -767,11 +771,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
         }
         M = mn;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;          // 0: a row without a key; NaN goes out
     const size_t orow = (size_t)unit * a.G * a.n + row;
     *reinterpret_cast<uint2 *>(a.out + orow * D + c_lo) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (a.lse && c_lo == 0) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (a.lse && c_lo == 0) a.lse[orow] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 bool make_map(CUtensorMap *map, const void *base, uint64_t rows, int d, int box_rows) {

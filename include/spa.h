@@ -576,8 +576,10 @@ spa_status spa_rope_append(const void *q, const spa_strides *q_str, void *q_out,
  *             overwritten; calls that may overlap in time need one each
  *   out     : [B, Hq, n, d] bf16;  lse : [B, Hq, n] fp32 or NULL (natural log)
  * P is rounded to bf16 for the PV product, as in spa_sparse_attn_prefill; sums and
- * the softmax state are fp32. A non-finite value in a kept block or a used node's row
- * may reach every query of its kv-head.
+ * the softmax state are fp32. A query that meets a NaN score, or one of +inf, gets NaN
+ * in out and lse, as in the formula (out = 0 with lse = -inf is only ever a row without
+ * keys); a non-finite value in a kept block or a used node's row may reach every query
+ * of its kv-head.
  */
 size_t spa_tree_workspace_bytes(int B, int Hq, int Hkv, int n, int T, int d, int block);
 spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, spa_dtype dt, int B,

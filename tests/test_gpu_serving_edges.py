@@ -1,0 +1,67 @@
+"""The serving operators at the edges of what their documentation allows: values that are
+not finite, tensors that start anywhere, drafted rows, trees with branches. Helpers and
+tolerances are those of test_gpu_serving."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_long_stats_b200 as spa
+from tests.test_gpu_serving import (BF, U, gen, ok, randn, ref_tree, tree_of)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+# one tile per run, so that every unit is joined; and units that one run finishes
+@pytest.mark.parametrize("B,Hq,Hkv,n,T", [(1, 4, 2, 5, 700), (80, 8, 4, 3, 140), (1, 10, 1, 33, 1300)])
+@pytest.mark.parametrize("where", ["query", "text key", "drafted key", "infinite key", "text value"])
+def test_tree_gives_what_the_definition_does_for_values_that_are_not_finite(B, Hq, Hkv, n, T, where):
+    g = gen(T + n)
+    q, kc, vc = randn(g, B, Hq, n, 128), randn(g, B, Hkv, T, 128), randn(g, B, Hkv, T, 128)
+    parents = tree_of(g, B, n)
+    parents[:, -1] = -2                               # an unused node: never touched
+    clean, clean_lse = spa.spa_sparse_attn_tree(q, kc, vc, parents, 64, None, None, 0.09, want_lse=True)
+    P, hit = T - n, torch.zeros(B, Hq, n, dtype=torch.bool, device="cuda")
+    G = Hq // Hkv
+    if where == "query":
+        q[0, 1, 1, 7] = math.nan
+        hit[0, 1, 1] = True
+    elif where == "text key":
+        kc[-1, 0, P // 2, 3] = math.nan
+        hit[-1, :G] = True
+    elif where == "drafted key":                      # node 0: its descendants see it
+        kc[-1, -1, P, 3] = math.nan
+        for i in range(n):
+            j = i
+            while j > 0:
+                j = int(parents[-1, j])
+            hit[-1, -G:, i] = j == 0
+    elif where == "infinite key":                     # +inf and -inf scores, by the query's sign
+        kc[0, 0, 0, 11] = math.inf
+        q[0, :G, 0, 11], q[0, :G, 1, 11] = 2.0, -2.0
+        q[0, :G, :, 11] += (q[0, :G, :, 11] == 0).to(BF)
+        hit[0, :G] = q[0, :G, :, 11] > 0
+    else:
+        vc[0, 0, 0, 5] = math.inf
+    hit &= (parents >= -1)[:, None]
+    out, lse = spa.spa_sparse_attn_tree(q, kc, vc, parents, 64, None, None, 0.09, want_lse=True)
+    ok()
+    if where == "text value":                         # lse without a trace, one feature infinite
+        assert torch.equal(lse, clean_lse)
+        live = (parents[0] >= -1).expand(G, n)
+        assert bool((out[0, :G, :, 5][live] == math.inf).all())
+        out[0, :G, :, 5] = clean[0, :G, :, 5]
+        assert torch.equal(out, clean)
+        return
+    assert bool(hit.any()) and bool(torch.isnan(lse[hit]).all()) and bool(torch.isnan(out[hit]).all())
+    rest = ~hit
+    if where == "infinite key":                       # a score of -inf: a key without weight
+        assert bool(torch.isfinite(out[rest].float()).all())
+        want, wl, mag, qk = ref_tree(q[:1, :G], kc[:1, :1, 1:], vc[:1, :1, 1:], parents[:1], 64, None, 0.09, None)
+        d, r = 2.0 ** -17 * qk + 2.0 ** -18, (rest & (parents >= -1)[:, None])[:1, :G]
+        tol = (1.02 * U + 2 * d[..., None]) * mag + U * want.abs()
+        assert bool(r.any()) and bool(((out[:1, :G].double() - want).abs() <= tol)[r].all())
+    else:
+        assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
