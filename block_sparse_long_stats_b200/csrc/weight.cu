@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Pair sh_pair;
     __shared__ long long sh_total;
     __shared__ __align__(16) float nl_s[kGroups][COLS]; // -lse of the columns, log2 units
+    __shared__ __align__(16) uint32_t dead_s[kGroups][4];   // columns of queries that saw nothing
     __shared__ float red[STREAM ? kUnits : 1][kGroups][kTile];   // sums of the last key tiles
     __shared__ int arrived[STREAM ? kUnits : 1][4];              // warps that have brought theirs
 
@@ -523,8 +524,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (fresh) {
                 named_bar_sync(2 + wg, 128);           // the group is done with the last columns
-                if (r < COLS) nl_s[wg][r] = minus_log2(a.nqt > 1 ? nl : column(at));
+                const float lse = a.nqt > 1 ? nl : column(at);
+                const unsigned dead =
+                    __ballot_sync(0xffffffffu, col && at.qi * a.pc + ci < a.Lq && lse == -INFINITY);
+                if (r < COLS) nl_s[wg][r] = minus_log2(lse);
+                if (lane == 0) dead_s[wg][warp & 3] = dead;
                 named_bar_sync(2 + wg, 128);
+            }
+            // a query that saw nothing may hold anything (columns without a row hold zeros)
+            const uint4 dead = *reinterpret_cast<const uint4 *>(dead_s[wg]);
+            if ((dead.x | dead.y | dead.z | dead.w) != 0u) {
+                if (!masked) see[0] = see[1] = see[2] = see[3] = 0xffffffffu;
+                masked = true;
+                see[0] &= ~dead.x;
+                see[1] &= ~dead.y;
+                see[2] &= ~dead.z;
+                see[3] &= ~dead.w;
             }
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (uint32_t)((mc / BUFS) & 1), a.err));
             if (ok) {
@@ -688,6 +703,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
     };
     uint32_t qf[NT][KB][4];
     float nl[NT][2];
+    uint32_t saw = 0;                            // bit 2 t + e: that column's query saw a key
     bool fresh = true;
     hm[0] = heads_of(bg, sl);
     load(bg, sl, hm[0], kr[0], pr[0]);
@@ -696,6 +712,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
         for (int now = 0; now < 2; ++now) {      // unrolled so that the two buffers stay registers
             if (fresh) {                         // a new (b, kv-head): its rows lie together in q and lse
                 fresh = false;
+                saw = 0;
                 const size_t row0 = (size_t)bg * rows;
                 const uint4 *q4 = static_cast<const uint4 *>(a.q);
 #pragma unroll
@@ -713,7 +730,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int c = t * 8 + 2 * tq + e;
-                        nl[t][e] = c < rows ? minus_log2(__ldg(a.lse + row0 + c)) : -INFINITY;
+                        const float lse = c < rows ? __ldg(a.lse + row0 + c) : -INFINITY;
+                        nl[t][e] = minus_log2(lse);
+                        if (lse != -INFINITY) saw |= 1u << (2 * t + e);
                     }
                 }
             }
@@ -776,8 +795,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
                         if (mk)
                             heads = ci[t][e] < a.Lq && ch[t][e] < a.G
                                         ? mk[(size_t)(at / a.block - off / a.block) * a.nbp] : 0u;
-                        const bool in = (heads >> ch[t][e]) & 1u;
-                        // keys behind the sequence may hold anything: select
+                        const bool in = (heads >> ch[t][e]) & (saw >> (2 * t + e)) & 1u;
+                        // keys behind the sequence and queries that saw nothing may hold anything: select
                         const float y0 = fmaf(c[t][0][e] + c[t][1][e], a.scale_log2, nl[t][e]);
                         const float y1 = fmaf(c[t][0][2 + e] + c[t][1][2 + e], a.scale_log2, nl[t][e]);
                         w0 += in && t0 <= at ? fast_exp2(y0) : 0.f;

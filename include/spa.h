@@ -600,7 +600,7 @@ spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, s
  *         1 <= Lq <= T, at most 16 query heads per kv-head
  *   lse : [B, Hq, Lq] fp32, natural: what spa_sparse_attn_prefill or
  *         spa_sparse_attn_tree wrote for the same queries, keys and lists. A row of
- *         -inf (it saw nothing) adds nothing.
+ *         -inf (it saw nothing) adds nothing, whatever its query holds.
  *   lens : device int32 [B], Lq <= lens[b] <= T, or NULL: T. Outside: clamped, recorded
  *         as SPA_DEVERR_BAD_COUNT. Keys from lens[b] on get no weight (out = decay
  *         prev), whatever their rows hold.

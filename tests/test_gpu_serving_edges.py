@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import block_sparse_long_stats_b200 as spa
-from tests.test_gpu_serving import (BF, U, gen, ok, randn, ref_tree, tree_of)
+from tests.test_gpu_serving import (BF, SCALE, U, gen, ok, randn, ref_tree, tree_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,38 @@ def test_tree_gives_what_the_definition_does_for_values_that_are_not_finite(B, H
         assert bool(r.any()) and bool(((out[:1, :G].double() - want).abs() <= tol)[r].all())
     else:
         assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+
+
+# one query tile per head in registers, 64 and 128 columns, and streams of query tiles
+@pytest.mark.parametrize("Hq,Hkv,Lq,T,d,block,p", [
+    (8, 2, 1, 1000, 128, 16, None), (8, 2, 4, 515, 64, 32, 0.6), (8, 2, 13, 700, 128, 64, None),
+    (8, 2, 31, 900, 64, 64, 0.5), (5, 1, 25, 400, 128, 128, None), (8, 2, 130, 1111, 128, 64, None),
+    (10, 2, 130, 1111, 64, 128, 0.5), (4, 4, 700, 700, 128, 128, None)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_query_that_saw_nothing_adds_nothing_whatever_it_holds(Hq, Hkv, Lq, T, d, block, p, bad):
+    g = gen(T + Lq + Hq)
+    q, k = randn(g, 2, Hq, Lq, d), randn(g, 2, Hkv, T, d)
+    idx = count = None
+    if p is not None:
+        nb, nq = -(-T // block), (T - 1) // block - (T - Lq) // block + 1
+        keep = torch.rand(2, Hq, nq, nb, generator=g, device="cuda") < p
+        j = torch.arange(nb, device="cuda", dtype=torch.int32)
+        idx = torch.where(keep, j, nb).sort(dim=3).values.to(torch.int32).contiguous()
+        count = keep.sum(3).to(torch.int32)
+    lse = torch.randn(2, Hq, Lq, generator=g, device="cuda") + math.log(T)
+    dead = torch.rand(2, Hq, Lq, generator=g, device="cuda") < 0.3
+    dead[0, 0, 0] = dead[1, -1, -1] = True
+    lse[dead] = -math.inf
+    q[dead] = 0.0
+    want = spa.spa_attn_weight(q, k, lse, SCALE[d], block, idx, count)
+    q[dead] = bad
+    q[0, 0, 0, 1:] = 0.0                              # one feature is enough
+    got = spa.spa_attn_weight(q, k, lse, SCALE[d], block, idx, count)
+    ok()
+    assert bool(torch.isfinite(want).all()) and torch.equal(got, want)
+    lse[0, 0, 0] = 1.0                                # a query that saw keys is not hidden
+    got = spa.spa_attn_weight(q, k, lse, SCALE[d], block, idx, count)
+    if p is None and math.isnan(bad):
+        assert bool(torch.isnan(got[0, 0, 0]))
+    assert torch.equal(got[1], want[1])
+    ok()
