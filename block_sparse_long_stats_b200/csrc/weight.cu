@@ -752,11 +752,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
                 }
                 hm[now ^ 1] = heads_of(bg2, sl2);
                 load(bg2, sl2, hm[now ^ 1], kr[now ^ 1], pr[now ^ 1]);
-                // and the slabs after it into L2, a line per lane
+                // and the slabs after it into L2, a line per lane (a cut slab: its rows in the cache)
                 const int far = sl2 + kFar;
                 if (far < ns2 && (far - sl2) < left) {
                     const int at = one ? far - ahead_at : 0;
-                    if (at < 32 && (!one || __shfl_sync(0xffffffffu, ahead, at)) && lane < kSlab * D * 2 / 128)
+                    const int lines = min(kSlab, a.T - far * kSlab) * (D * 2 / 128);
+                    if (at < 32 && (!one || __shfl_sync(0xffffffffu, ahead, at)) && lane < lines)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(
                             reinterpret_cast<const char *>(k4) + (((size_t)bg2 * a.T + far * kSlab) * D * 2 + lane * 128)));
                 }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import block_sparse_long_stats_b200 as spa
-from tests.test_gpu_serving import (BF, SCALE, U, gen, ok, randn, ref_tree, tree_of)
+from tests.test_gpu_serving import (BF, SCALE, U, gen, ok, randn, ref_tree, ref_weight, tree_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,16 @@ def test_a_query_that_saw_nothing_adds_nothing_whatever_it_holds(Hq, Hkv, Lq, T,
         assert bool(torch.isnan(got[0, 0, 0]))
     assert torch.equal(got[1], want[1])
     ok()
+
+
+@pytest.mark.parametrize("T", [17, 33, 4095, 4097, 4111])
+@pytest.mark.parametrize("Lq,d", [(1, 128), (2, 64)])
+def test_weight_of_a_cache_that_ends_inside_a_slab(T, Lq, d):
+    # the last slab of 16 keys is cut by the end of the tensor
+    g = gen(T + d)
+    q, k = randn(g, 2, 4, Lq, d), randn(g, 2, 2, T, d)
+    lse = torch.randn(2, 4, Lq, generator=g, device="cuda") + math.log(T)
+    got = spa.spa_attn_weight(q, k, lse, SCALE[d])
+    ok()
+    want, tol = ref_weight(q, k, lse, SCALE[d], 128, None, None, None, 1.0)
+    assert bool(((got.double() - want).abs() <= tol).all())
