@@ -941,15 +941,34 @@ def decode_tree(q, kc, vc, parents, block: int, top_p: float, mean=None, var=Non
     """One step over a tree of n drafted tokens, in the last n rows of the caches: (stats, if
     not given) -> selection by node 0's query -> tree attention over the kept blocks.
 
-    Returns dict(out, lse, idx, count, mean, var).
+    The T - n rows before the tree are the committed text, and the selection is of their
+    blocks alone: the last n_local of them are kept, and the drafted rows, which the tree
+    attends to anyway, take no part. mean and var are the statistics of those rows' blocks
+    (more blocks may follow: they are not read). The tree of one node is a decode step:
+    selected as by decode(), over all T rows.
+    Returns dict(out, lse, idx, count, mean, var), mean and var those of the selection.
     """
-    T = kc.shape[2]
-    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    B, Hq, n, d = q.shape
+    Hkv, T = kc.shape[1], kc.shape[2]
+    text = T if n == 1 else max(T - n, 0)
+    nb, cap = -(-text // block), -(-T // block)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
     with _On(q, stream):
-        root = q[:, :, :1].contiguous()
         if mean is None or var is None:
-            mean, var = spa_block_stats(kc, block)
-        idx, count = spa_select(root, mean, var, T, block, scale, top_p, n_sink, n_local, k_min)
+            whole = text // block if text < T else cap           # blocks without a drafted row
+            mean, var = spa_block_stats(kc, block, 0, whole)
+            if whole < nb:                                       # the text's last block, cut at its end
+                tail = spa_block_stats(kc[:, :, whole * block:text].contiguous(), block)
+                mean[:, :, whole:nb], var[:, :, whole:nb] = tail
+        elif mean.shape[2] < nb or var.shape[2] < nb:
+            raise ValueError(f"mean and var must hold the {nb} blocks of the {text} rows before the tree")
+        mean, var = mean[:, :, :nb].contiguous(), var[:, :, :nb].contiguous()
+        if text > 0:
+            idx, count = spa_select(q[:, :, :1].contiguous(), mean, var, text, block, scale, top_p, n_sink,
+                                    n_local, k_min, cap=cap)
+        else:
+            idx = torch.zeros((B, Hq, 1, cap), device=q.device, dtype=torch.int32)
+            count = torch.zeros((B, Hq, 1), device=q.device, dtype=torch.int32)
         out, lse = spa_sparse_attn_tree(q, kc, vc, parents, block, idx, count, scale,
                                         workspace=workspace, want_lse=want_lse)
     return {"out": out, "lse": lse, "idx": idx, "count": count, "mean": mean, "var": var}

@@ -570,8 +570,10 @@ spa_status spa_rope_append(const void *q, const spa_strides *q_str, void *q_out,
  *             the rows of unused nodes, may hold anything, NaN included.
  *   idx, count : [B, Hq, 1, cap], [B, Hq, 1] ascending lists of blocks of `block` keys (16,
  *             32, 64 or 128), as spa_select gives them with Lq = 1 (cap >= ceil(T/block)),
- *             one list for all nodes; both NULL: every block. Blocks at or after len
- *             are allowed and add nothing.
+ *             one list for all nodes; both NULL: every block. The lists are of the text
+ *             before the tree: blocks at or after len are allowed and add nothing, so
+ *             a selection over rows of the tree would spend its n_local blocks and its
+ *             top_p on them.
  *   workspace : >= spa_tree_workspace_bytes(...) device bytes, 16-byte aligned,
  *             overwritten; calls that may overlap in time need one each
  *   out     : [B, Hq, n, d] bf16;  lse : [B, Hq, n] fp32 or NULL (natural log)

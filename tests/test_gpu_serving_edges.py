@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import block_sparse_long_stats_b200 as spa
-from tests.test_gpu_serving import (BF, SCALE, U, gen, ok, randn, ref_tree, ref_weight, tree_of)
+from tests.test_gpu_serving import (BF, SCALE, U, check_tree, gen, lists, ok, randn, ref_tree, ref_weight, tree_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,51 @@ def test_weight_of_a_cache_that_ends_inside_a_slab(T, Lq, d):
     ok()
     want, tol = ref_weight(q, k, lse, SCALE[d], 128, None, None, None, 1.0)
     assert bool(((got.double() - want).abs() <= tol).all())
+
+
+# ---------------------------------------------------------------- drafted rows
+
+@pytest.mark.parametrize("n,T,block", [(64, 1024, 16), (64, 1030, 16), (33, 1500, 32), (2, 1001, 16), (128, 700, 64)])
+def test_decode_tree_selects_from_the_committed_text(n, T, block):
+    g = gen(T + n)
+    B, Hq, Hkv, P = 2, 8, 2, T - n
+    q, kc, vc = randn(g, B, Hq, n, 128), randn(g, B, Hkv, T, 128), randn(g, B, Hkv, T, 128)
+    parents = tree_of(g, B, n)
+    r = spa.decode_tree(q, kc, vc, parents, block, 0.6, want_lse=True)
+    ok()
+    nb, kept = -(-P // block), torch.zeros(B, Hq, 1, -(-T // block) + 1, dtype=torch.bool, device="cuda")
+    assert r["idx"].shape[3] >= -(-T // block)
+    at = torch.arange(r["idx"].shape[3], device="cuda") < r["count"][..., None]
+    kept.scatter_(3, torch.where(at, r["idx"], kept.shape[3] - 1).long(), at)
+    kept = kept[..., :-1]
+    assert bool(kept[..., nb - 1].all()) and bool(kept[..., 0].all()) and not bool(kept[..., nb:].any())
+    # the lists of the text alone, its newest row as the position
+    m, v = spa.spa_block_stats(kc[:, :, :P].contiguous(), block)
+    i, c = spa.spa_select(q[:, :, :1].contiguous(), m, v, P, block, 128.0 ** -0.5, 0.6)
+    assert torch.equal(c, r["count"]) and torch.equal(i[at[..., :nb]], r["idx"][at])
+    assert torch.equal(m, r["mean"]) and torch.equal(v, r["var"])
+    check_tree(q, kc, vc, parents, block, kept, 128.0 ** -0.5, None, r["out"], r["lse"])
+    # whatever the drafted rows hold; with the statistics given, of the text or of more blocks
+    kc[:, :, P:] = 30.0
+    more = [torch.cat((x, torch.full((B, Hkv, 3, 128), math.nan, device="cuda")), 2) for x in (m, v)]
+    for kw in ({}, dict(mean=m, var=v), dict(mean=more[0], var=more[1])):
+        s = spa.decode_tree(q, kc, vc, parents, block, 0.6, **kw)
+        assert torch.equal(s["count"], r["count"]) and torch.equal(s["idx"][at], r["idx"][at])
+    ok()
+
+
+def test_decode_tree_without_text_and_of_one_node():
+    g = gen(31)
+    q, kc, vc = randn(g, 2, 8, 20, 128), randn(g, 2, 2, 20, 128), randn(g, 2, 2, 20, 128)
+    parents = tree_of(g, 2, 20)
+    r = spa.decode_tree(q, kc, vc, parents, 16, 0.6, want_lse=True)
+    ok()
+    assert int(r["count"].sum()) == 0
+    check_tree(q, kc, vc, parents, 16, None, 128.0 ** -0.5, None, r["out"], r["lse"])
+    for T in (1000, 1025):                            # the tree of one node is a decode step
+        q, kc, vc = randn(g, 2, 8, 1, 128), randn(g, 2, 2, T, 128), randn(g, 2, 2, T, 128)
+        one = torch.full((2, 1), -1, device="cuda", dtype=torch.int32)
+        a, b = spa.decode_tree(q, kc, vc, one, 32, 0.6), spa.decode(q, kc, vc, 32, 0.6)
+        at = torch.arange(a["idx"].shape[3], device="cuda") < a["count"][..., None]
+        assert torch.equal(a["count"], b["count"]) and torch.equal(a["idx"][at], b["idx"][at])
+    ok()
