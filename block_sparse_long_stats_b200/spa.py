@@ -789,7 +789,9 @@ def spa_attn_weight(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, scale: 
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """Attention weight that the sequence's last Lq queries, q [B,Hq,Lq,d] with their lse
-    [B,Hq,Lq], give every key of k [B,Hkv,T,d], added to decay * prev: [B,Hkv,T] fp32."""
+    [B,Hq,Lq], give every key of k [B,Hkv,T,d], added to decay * prev: [B,Hkv,T] fp32. The
+    lse has to be over the keys that a query sees here: prefill's, or that of a tree's root
+    or chain (of a tree with branches: of the accepted path, its rows copied together)."""
     B, Hq, Lq, d = q.shape
     Hkv, T = k.shape[1], k.shape[2]
     dev, dt = q.get_device(), q.dtype

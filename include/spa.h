@@ -600,9 +600,16 @@ spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, s
  * where lists are given).
  *   q   : [B, Hq, Lq, d];  k : [B, Hkv, T, d];  dt = SPA_BF16, d = 64 or 128,
  *         1 <= Lq <= T, at most 16 query heads per kv-head
- *   lse : [B, Hq, Lq] fp32, natural: what spa_sparse_attn_prefill or
- *         spa_sparse_attn_tree wrote for the same queries, keys and lists. A row of
- *         -inf (it saw nothing) adds nothing, whatever its query holds.
+ *   lse : [B, Hq, Lq] fp32, natural: each query's log-sum-exp over the keys that it sees
+ *         here. That is what spa_sparse_attn_prefill wrote for the same queries, keys and
+ *         lists, and what spa_sparse_attn_tree wrote for nodes whose ancestors are the rows
+ *         right before them: the root (Lq = 1, lens = its row + 1) or a chain (parents
+ *         i - 1). The weight knows no tree. Of one with branches first copy the accepted
+ *         path's rows of K and V together (row len + path[i] to len + i), then take the
+ *         path's queries and lse; node by node it would credit the rows between them. With
+ *         lists, every block from len / block on has to be on them: a tree sees its own
+ *         rows whether their blocks are listed or not. A row of -inf (it saw nothing) adds
+ *         nothing, whatever its query holds.
  *   lens : device int32 [B], Lq <= lens[b] <= T, or NULL: T. Outside: clamped, recorded
  *         as SPA_DEVERR_BAD_COUNT. Keys from lens[b] on get no weight (out = decay
  *         prev), whatever their rows hold.

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import block_sparse_long_stats_b200 as spa
-from tests.test_gpu_serving import (BF, SCALE, U, check_tree, gen, lists, ok, randn, ref_tree, ref_weight, tree_of)
+from tests.test_gpu_serving import (BF, E, SCALE, U, check_tree, gen, lists, ok, randn, ref_tree, ref_weight,
+                                    tree_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +162,60 @@ def test_decode_tree_without_text_and_of_one_node():
         at = torch.arange(a["idx"].shape[3], device="cuda") < a["count"][..., None]
         assert torch.equal(a["count"], b["count"]) and torch.equal(a["idx"][at], b["idx"][at])
     ok()
+
+
+# ---------------------------------------------------------------- from a tree to the accumulated weight
+
+def check_shares(q, kc, lse, scale, block, keep, lens, w):
+    """w is the queries' weight on the keys they attended to: key by key, and one in all for
+    each query and head."""
+    want, tol = ref_weight(q, kc, lse, scale, block, keep, lens, None, 1.0)
+    assert bool(((w.double() - want).abs() <= tol).all())
+    # the log-sum-exp's own error: 2^-17 of |q||k| summed over the features and 2^-18, 4 E of its size
+    G, Lq = q.shape[1] // kc.shape[1], q.shape[2]
+    k = kc.double().abs().nan_to_num().repeat_interleave(G, 1)
+    d = 2.0 ** -17 * scale * (q.double().abs() @ k.transpose(2, 3)).amax(3) + 2.0 ** -18 + 4 * E * lse.double().abs()
+    slack = tol.sum(2) + 2 * d.reshape(*w.shape[:2], -1).sum(2)
+    assert bool(((w.double().sum(2) - G * Lq).abs() <= slack).all())
+
+
+@pytest.mark.parametrize("n,block", [(1, 32), (9, 16), (40, 16), (40, 64)])
+def test_weight_of_a_chain_over_lists_sums_to_its_queries(n, block):
+    # drafts in a line; the lists get the blocks that the drafts lie in
+    g = gen(n + block)
+    B, Hq, Hkv, T = 2, 8, 2, 1003
+    P, nb = T - n, -(-T // block)
+    q, kc, vc = randn(g, B, Hq, n, 128), randn(g, B, Hkv, T, 128), randn(g, B, Hkv, T, 128)
+    parents = (torch.arange(n, device="cuda", dtype=torch.int32) - 1).expand(B, n).contiguous()
+    r = spa.decode_tree(q, kc, vc, parents, block, 0.5, want_lse=True)
+    j = torch.arange(nb, device="cuda")
+    keep = torch.zeros(B, Hq, 1, nb + 1, dtype=torch.bool, device="cuda")
+    at = torch.arange(r["idx"].shape[3], device="cuda") < r["count"][..., None]
+    keep = keep.scatter_(3, torch.where(at, r["idx"], nb).long(), at)[..., :nb] | (j >= P // block)
+    nq = (T - 1) // block - P // block + 1
+    keep = keep.expand(B, Hq, nq, nb)
+    idx = torch.where(keep, j, nb).sort(dim=3).values.to(torch.int32).contiguous()
+    w = spa.spa_attn_weight(q, kc, r["lse"], 128.0 ** -0.5, block, idx, keep.sum(3).to(torch.int32))
+    ok()
+    check_shares(q, kc, r["lse"], 128.0 ** -0.5, block, keep, None, w)
+
+
+def test_weight_of_an_accepted_path_and_of_the_root_sums_to_its_queries():
+    # a tree with branches in ragged caches: the root as it is, the path once its rows follow
+    # one another
+    g = gen(61)
+    B, Hq, Hkv, T, n, scale = 3, 8, 2, 600, 7, 128.0 ** -0.5
+    q, kc, vc = randn(g, B, Hq, n, 128), randn(g, B, Hkv, T, 128), randn(g, B, Hkv, T, 128)
+    parents = torch.tensor([[-1, 0, 0, 1, 2, 4, 2]] * B, device="cuda", dtype=torch.int32)
+    lens = torch.tensor([0, 77, T - n], device="cuda", dtype=torch.int32)
+    out, lse = spa.spa_sparse_attn_tree(q, kc, vc, parents, 64, None, None, scale, lens=lens, want_lse=True)
+    q1, lse1 = q[:, :, :1].contiguous(), lse[:, :, :1].contiguous()
+    check_shares(q1, kc, lse1, scale, 64, None, lens + 1, spa.spa_attn_weight(q1, kc, lse1, scale, lens=lens + 1))
+    path = torch.tensor([0, 2, 4, 5], device="cuda")
+    b = torch.arange(B, device="cuda")[:, None]
+    for c in (kc, vc):
+        c[b, :, lens[:, None] + torch.arange(4, device="cuda")] = c[b, :, lens[:, None] + path]
+    qp, lp = q[:, :, path].contiguous(), lse[:, :, path].contiguous()
+    w = spa.spa_attn_weight(qp, kc, lp, scale, lens=lens + 4)
+    ok()
+    check_shares(qp, kc, lp, scale, 64, None, lens + 4, w)
