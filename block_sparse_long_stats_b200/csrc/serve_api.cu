@@ -25,6 +25,7 @@ spa_status launched(cudaError_t e, const char *what) {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 spa_strides strides_or_dense(const spa_strides *s, int H, int L, int d) {
     if (s) return *s;
@@ -222,9 +223,10 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
     if (Lq > T) return fail(SPA_ERR_INVALID, "the queries are the sequence's last: Lq must be <= T");
     if (!(scale > 0.f) || !isfinite(scale)) return fail(SPA_ERR_INVALID, "scale must be > 0");
     if (!isfinite(decay)) return fail(SPA_ERR_INVALID, "decay must be finite");
-    if (!aligned16(q) || !aligned16(k) || !aligned16(lse) || !aligned16(prev) || !aligned16(out) ||
-        !aligned16(workspace))
-        return fail(SPA_ERR_INVALID, "tensors must be 16-byte aligned");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(workspace))
+        return fail(SPA_ERR_INVALID, "q, k and the workspace must be 16-byte aligned");
+    if (!aligned4(lse) || !aligned4(prev) || !aligned4(out))
+        return fail(SPA_ERR_INVALID, "tensors must be aligned to their elements");
     if (dt != SPA_BF16) return fail(SPA_ERR_UNSUPPORTED, "the accumulated weight is bf16 only");
     if (d != 64 && d != 128) return fail(SPA_ERR_UNSUPPORTED, "d must be 64 or 128");
     if (Hq / Hkv > 16) return fail(SPA_ERR_UNSUPPORTED, "at most 16 query heads per kv-head");

@@ -618,7 +618,8 @@ spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, s
  *         prefill for Lq = T, of decode for Lq = 1. With lists, lens has to be NULL or
  *         Lq = 1. cap >= ceil(T/block). block: 16, 32, 64 or 128 (read with lists only)
  *   prev : [B, Hkv, T] fp32 or NULL (zero);  decay : finite
- *   out  : [B, Hkv, T] fp32, may be prev
+ *   out  : [B, Hkv, T] fp32, may be prev. lse, prev and out may start at any element (a
+ *         batch slice); q and k are 16-byte aligned
  *   workspace : >= spa_attn_weight_workspace_bytes(...) device bytes (block = 0 there:
  *         without lists), 16-byte aligned, overwritten; calls that may overlap in time
  *         need one each

@@ -219,3 +219,23 @@ def test_weight_of_an_accepted_path_and_of_the_root_sums_to_its_queries():
     w = spa.spa_attn_weight(qp, kc, lp, scale, lens=lens + 4)
     ok()
     check_shares(qp, kc, lp, scale, 64, None, lens + 4, w)
+
+
+# ---------------------------------------------------------------- tensors that start anywhere
+
+def test_weight_takes_fp32_tensors_that_start_at_any_element():
+    g = gen(41)
+    for Lq, T in ((1, 515), (33, 301), (200, 777)):
+        q, k = randn(g, 3, 3, Lq, 128), randn(g, 3, 1, T, 128)
+        lse = torch.randn(3, 3, Lq, generator=g, device="cuda") + math.log(T)
+        prev = torch.rand(3, 1, T, generator=g, device="cuda")
+        want = spa.spa_attn_weight(q, k, lse, 0.09, prev=prev, decay=0.5)
+        out = torch.full_like(prev, 7.0)
+        for b in range(3):                            # batch slices: 4-byte aligned
+            spa.spa_attn_weight(q[b:b + 1].contiguous(), k[b:b + 1].contiguous(), lse[b:b + 1], 0.09,
+                                prev=prev[b:b + 1], decay=0.5, out=out[b:b + 1])
+        ok()
+        for b in range(3):
+            ww, tol = ref_weight(q[b:b + 1], k[b:b + 1], lse[b:b + 1], 0.09, 128, None, None, prev[b:b + 1], 0.5)
+            assert bool(((out[b:b + 1].double() - ww).abs() <= tol).all())
+            assert bool(((want[b:b + 1].double() - ww).abs() <= tol).all())
