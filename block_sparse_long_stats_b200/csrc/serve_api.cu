@@ -32,6 +32,17 @@ spa_strides strides_or_dense(const spa_strides *s, int H, int L, int d) {
     return spa_strides{(int64_t)H * L * d, (int64_t)L * d, d};
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Whether the rows of an output are each its own (no broadcast stride).
+bool own_rows(const spa_strides &s, int B, int H, int L) {
+    return (B == 1 || s.b) && (H == 1 || s.h) && (L == 1 || s.l);
+}
+
 bool block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
 
 spa_status check_rope(const RopeCall &c, spa_dtype dt, int Hq, int Hkv, spa_rope_layout layout) {
@@ -125,6 +136,8 @@ SPA_API spa_status spa_rope(const void *q, const spa_strides *q_str, void *q_out
     c.pos0 = pos0;
     const spa_status st = check_rope(c, dt, Hq, k ? Hkv : 0, layout);
     if (st != SPA_OK) return st;
+    if (q_out == k_out || !own_rows(c.t[0].ys, B, Hq, L) || (k && !own_rows(c.t[1].ys, B, Hkv, L)))
+        return fail(SPA_ERR_INVALID, "the rows of the outputs must not overlap");
     return launched(launch_rope(c, static_cast<cudaStream_t>(stream)), "rope launch");
 }
 
@@ -158,6 +171,9 @@ SPA_API spa_status spa_rope_append(const void *q, const spa_strides *q_str, void
     c.pos0 = rows ? 0 : row0;
     const spa_status st = check_rope(c, dt, Hq, Hkv, layout);
     if (st != SPA_OK) return st;
+    const size_t cache_bytes = (size_t)B * Hkv * T * d * (c.bf16 ? 2 : 4);
+    if (overlap(kc, cache_bytes, vc, cache_bytes) || !own_rows(c.t[0].ys, B, Hq, L))
+        return fail(SPA_ERR_INVALID, "the rows of the outputs must not overlap");
     c.err = device_error_word();
     if (!c.err) return fail(SPA_ERR_CUDA, "device error word unavailable");
     return launched(launch_rope(c, static_cast<cudaStream_t>(stream)), "rope launch");
@@ -243,6 +259,9 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
     }
     if (workspace_bytes < weight_workspace_bytes(B, Hkv, Lq, T, idx ? block : 0))
         return fail(SPA_ERR_INVALID, "workspace smaller than spa_attn_weight_workspace_bytes");
+    const size_t out_bytes = (size_t)B * Hkv * T * sizeof(float);
+    if (prev && prev != out && overlap(prev, out_bytes, out, out_bytes))
+        return fail(SPA_ERR_INVALID, "out may be prev, but not overlap it otherwise");
     int *err = device_error_word();
     if (!err) return fail(SPA_ERR_CUDA, "device error word unavailable");
     const WeightCall c{q, k, B, Hq, Hkv, Lq, T, d, idx ? block : 128, cap, lse, lens, idx, count,
@@ -279,14 +298,18 @@ SPA_API spa_status spa_cache_gather(const void *kc, const void *vc, const float 
         return fail(SPA_ERR_INVALID, "sizes must be positive");
     if (T_out < n_keep) return fail(SPA_ERR_INVALID, "T_out must be >= n_keep");
     if (dt != SPA_F32 && dt != SPA_BF16) return fail(SPA_ERR_INVALID, "unknown dtype");
-    if (kc == k_out || vc == v_out || kc == v_out || vc == k_out || (score && score == score_out))
-        return fail(SPA_ERR_INVALID, "the smaller cache must not overlap the cache");
     if (!aligned16(kc) || !aligned16(vc) || !aligned16(k_out) || !aligned16(v_out))
         return fail(SPA_ERR_INVALID, "tensors must be 16-byte aligned");
     const int row_bytes = d * (dt == SPA_BF16 ? 2 : 4);
     if (row_bytes % 16) return fail(SPA_ERR_UNSUPPORTED, "rows must be a multiple of 16 bytes");
     if ((long long)B * Hkv * n_keep * (row_bytes / 16) > (1ll << 39))
         return fail(SPA_ERR_UNSUPPORTED, "too many rows");
+    const size_t rows_in = (size_t)B * Hkv * T, rows_out = (size_t)B * Hkv * T_out;
+    const size_t in = rows_in * row_bytes, out = rows_out * row_bytes;
+    if (overlap(kc, in, k_out, out) || overlap(kc, in, v_out, out) || overlap(vc, in, k_out, out) ||
+        overlap(vc, in, v_out, out) || (overlap(k_out, out, v_out, out) && (kc != vc || k_out != v_out)) ||
+        (score && overlap(score, rows_in * sizeof(float), score_out, rows_out * sizeof(float))))
+        return fail(SPA_ERR_INVALID, "the smaller cache must not overlap the cache, nor its parts one another");
     int *err = device_error_word();
     if (!err) return fail(SPA_ERR_CUDA, "device error word unavailable");
     return launched(launch_cache_gather(kc, vc, score, B, Hkv, T, row_bytes, keep, n_keep, count, T_out,

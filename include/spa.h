@@ -515,7 +515,8 @@ typedef struct {
  *   so a fused projection's [B, L, heads, d] output is read in place
  *   q_out, k_out : the same shapes, with strides qo_str, ko_str (NULL: dense). An
  *            output may be its own input with the same strides; it must not overlap
- *            an input otherwise
+ *            an input otherwise, nor the other output, and a broadcast stride (0) is
+ *            SPA_ERR_INVALID in an output
  *   rot    : even, 2 <= rot <= d;  d <= 256
  *   freqs  : HOST array of rot/2 doubles, read before the call returns
  *   pos    : device int32 [B, L], any values, or NULL: row t is at pos0 + t
@@ -537,7 +538,7 @@ spa_status spa_rope(const void *q, const spa_strides *q_str, void *q_out,
  *   kc[b, g, row + t, :] = rotated k[b, g, t, :],  vc[b, g, row + t, :] = v[b, g, t, :]
  * with row = rows[b] (device int32 [B]) or, where rows is NULL, row0.
  *   v [B, Hkv, L, d] with strides v_str; kc, vc: [B, Hkv, T, d] dense, overlapping no
- *   input; every other row of the caches is left as it was. pos NULL: token t of
+ *   input and (SPA_ERR_INVALID) not one another; every other row of the caches is left as it was. pos NULL: token t of
  *   sequence b is at position row + t. A row outside [0, T) is not written and
  *   recorded as SPA_DEVERR_BAD_INDEX. Other arguments as spa_rope.
  */
@@ -618,7 +619,7 @@ spa_status spa_sparse_attn_tree(const void *q, const void *kc, const void *vc, s
  *         prefill for Lq = T, of decode for Lq = 1. With lists, lens has to be NULL or
  *         Lq = 1. cap >= ceil(T/block). block: 16, 32, 64 or 128 (read with lists only)
  *   prev : [B, Hkv, T] fp32 or NULL (zero);  decay : finite
- *   out  : [B, Hkv, T] fp32, may be prev. lse, prev and out may start at any element (a
+ *   out  : [B, Hkv, T] fp32, may be prev (a partial overlap is SPA_ERR_INVALID). lse, prev and out may start at any element (a
  *         batch slice); q and k are 16-byte aligned
  *   workspace : >= spa_attn_weight_workspace_bytes(...) device bytes (block = 0 there:
  *         without lists), 16-byte aligned, overwritten; calls that may overlap in time
@@ -660,7 +661,7 @@ spa_status spa_evict_select(const float *score, const int32_t *lens, int B, int 
  *            SPA_DEVERR_BAD_INDEX, a count outside [0, n_keep] clamped and recorded as
  *            SPA_DEVERR_BAD_COUNT.
  *   k_out, v_out : [B, Hkv, T_out, d], T_out >= n_keep; score_out : [B, Hkv, T_out]. They
- *            must not overlap the inputs (an exact same pointer is SPA_ERR_INVALID). Rows
+ *            must not overlap the inputs, nor (unless kc = vc) one another: SPA_ERR_INVALID. Rows
  *            from count[b] on are left as they were.
  * Keys keep the rotary positions they were written with; block statistics of the
  * smaller cache are those of spa_block_stats on it.
