@@ -94,6 +94,8 @@ struct WeightCall {
     float *out;
     int *err;
 };
+// Blocks of a list: the grid of the kernel that marks them has a row per 512.
+constexpr int kMaxMarkBlocks = 65534 * 512;
 size_t weight_workspace_bytes(int B, int Hkv, int Lq, int T, int block);
 cudaError_t launch_weight(const WeightCall &c, cudaStream_t s);
 

@@ -255,6 +255,7 @@ SPA_API spa_status spa_attn_weight(const void *q, const void *k, spa_dtype dt, i
         if (block <= 0) return fail(SPA_ERR_INVALID, "sizes must be positive");
         if (!block_ok(block)) return fail(SPA_ERR_UNSUPPORTED, "block must be 16, 32, 64 or 128");
         if (cap < (T + block - 1) / block) return fail(SPA_ERR_INVALID, "cap must be >= nb");
+        if (T / block > kMaxMarkBlocks) return fail(SPA_ERR_UNSUPPORTED, "too many blocks");
         if (lens && Lq != 1) return fail(SPA_ERR_INVALID, "lists of several queries need lens = NULL");
     }
     if (workspace_bytes < weight_workspace_bytes(B, Hkv, Lq, T, idx ? block : 0))
@@ -279,6 +280,7 @@ SPA_API spa_status spa_evict_select(const float *score, const int32_t *lens, int
     if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > n_keep)
         return fail(SPA_ERR_INVALID, "need n_sink, n_recent >= 0 and n_sink + n_recent <= n_keep");
     if ((long long)B * Hkv > (1 << 27)) return fail(SPA_ERR_UNSUPPORTED, "too many heads");
+    if (T > 0x7fffffff - 63) return fail(SPA_ERR_UNSUPPORTED, "too many keys");   // T is rounded up in 32 bits
     int *err = device_error_word();
     if (!err) return fail(SPA_ERR_CUDA, "device error word unavailable");
     return launched(launch_evict_select(score, lens, B, Hkv, T, n_keep, n_sink, n_recent, keep, count,

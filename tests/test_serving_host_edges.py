@@ -52,3 +52,10 @@ def test_broadcast_outputs_are_refused(lib):  # noqa: F811
     assert lib.spa_rope_append(FAKE, None, OTHER, ctypes.byref(Strides(512, 0, 128)), FAKE, None, FAKE, None,
                                0x100000, 0x200000, 1, 1, 4, 2, 1, 100, 128, 64, 0, freqs(64), 1.0, None, None, 0,
                                None) == 1
+
+
+def test_sizes_beyond_the_launch_and_the_index_arithmetic_are_refused(lib):  # noqa: F811
+    # 37.5 million blocks: more rows than a grid has; a T that is rounded up past 32 bits
+    T = 600_000_000
+    assert weight(lib, Hkv=1, T=T, d=64, cap=T // 16) == 2
+    assert lib.spa_evict_select(FAKE, None, 1, 1, 2 ** 31 - 1, 10, 4, 6, OTHER, OTHER + 4096, None) == 2
