@@ -854,18 +854,18 @@ def spa_cache_gather(kc: torch.Tensor, vc: torch.Tensor, keep: torch.Tensor,
                      k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                      score_out: torch.Tensor | None = None, stream=None):
     """The rows of kc, vc [B,Hkv,T,d] (and of score) that keep [B,Hkv,n_keep] names, closed up
-    in k_out, v_out [B,Hkv,T_out,d] (T_out >= n_keep; new ones of n_keep rows, zero behind
-    the last, where none are given). Returns (k_out, v_out, score_out or None)."""
+    in k_out, v_out [B,Hkv,T_out,d] (T_out >= n_keep; new ones of n_keep rows, or of k_out's,
+    zero behind the last, where none are given). Returns (k_out, v_out, score_out or None)."""
     B, Hkv, T, d = kc.shape
     n_keep = keep.shape[2]
     dev, dt = kc.get_device(), kc.dtype
 
     def call(st):
         nonlocal k_out, v_out, score_out
-        new = kc.new_zeros if count is not None else kc.new_empty
+        T_out = n_keep if k_out is None else k_out.shape[2]
+        new = kc.new_empty if count is None and T_out == n_keep else kc.new_zeros
         if k_out is None:
-            k_out = new((B, Hkv, n_keep, d))
-        T_out = k_out.shape[2]
+            k_out = new((B, Hkv, T_out, d))
         if v_out is None:
             v_out = new((B, Hkv, T_out, d))
         if score_out is None and score is not None:

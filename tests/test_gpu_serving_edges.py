@@ -239,3 +239,22 @@ def test_weight_takes_fp32_tensors_that_start_at_any_element():
             ww, tol = ref_weight(q[b:b + 1], k[b:b + 1], lse[b:b + 1], 0.09, 128, None, None, prev[b:b + 1], 0.5)
             assert bool(((out[b:b + 1].double() - ww).abs() <= tol).all())
             assert bool(((want[b:b + 1].double() - ww).abs() <= tol).all())
+
+
+def test_new_outputs_of_the_gather_are_zero_behind_the_list():
+    # k_out is given with more rows than the list; the new v_out and score_out have as many
+    g = gen(71)
+    kc, vc = randn(g, 2, 2, 60, 128), randn(g, 2, 2, 60, 128)
+    score = torch.rand(2, 2, 60, generator=g, device="cuda")
+    keep = torch.randint(0, 60, (2, 2, 7), generator=g, device="cuda", dtype=torch.int32)
+    for _ in range(3):                                # memory that held something else
+        junk = [torch.full((2, 2, 500, 128), 3.0, device="cuda", dtype=BF), torch.full((2, 2, 500), 3.0, device="cuda")]
+        del junk
+        k_out = torch.full((2, 2, 500, 128), 5.0, device="cuda", dtype=BF)
+        k, v, s = spa.spa_cache_gather(kc, vc, keep, score=score, k_out=k_out)
+        ok()
+        assert k is k_out and v.shape == k.shape and s.shape == (2, 2, 500)
+        assert bool((k[:, :, 7:] == 5).all() and (v[:, :, 7:] == 0).all() and (s[:, :, 7:] == 0).all())
+        at = keep.long()
+        assert torch.equal(v[:, :, :7], vc.gather(2, at[..., None].expand(2, 2, 7, 128)))
+        assert torch.equal(s[:, :, :7], score.gather(2, at))
