@@ -44,7 +44,6 @@ namespace {
 constexpr int kCtas = 296;             // two per SM
 constexpr int kThreads = 192;
 constexpr int kTile = 128;             // keys
-constexpr int kMinTiles = 1;           // tiles a run has at least
 constexpr int kRange = 1536;           // blocks whose list is held in shared memory
 constexpr int kShortList = 1024;       // entries up to which a list is read whole
 constexpr float kLog2e = 1.4426950408889634f;
@@ -99,7 +98,7 @@ __device__ __forceinline__ int run_total(const TreeArgs &a) {
     return __reduce_add_sync(0xffffffffu, s) * upb;
 }
 __device__ __forceinline__ int run_chunk(const TreeArgs &a, int total) {
-    return max(kMinTiles, (total + a.runs - 1) / a.runs);
+    return (total + a.runs - 1) / a.runs;
 }
 __device__ __forceinline__ Where locate(const TreeArgs &a, int pos) {
     const int lane = threadIdx.x & 31, upb = a.Hkv;
@@ -151,16 +150,6 @@ __device__ __forceinline__ int lower_bound(const int32_t *list, int cnt, int j) 
         if (hi < lo) hi = lo;
     }
     return lo;
-}
-
-// 16 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *x) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
-          "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
-        : "r"(taddr));
 }
 
 // What a CTA's roles share about the segment (the part of a run inside one unit) and the
@@ -802,12 +791,11 @@ cudaError_t launch_cfg(const TreeCall &c, TreeArgs a, cudaStream_t s) {
         return cudaErrorNotSupported;
     cudaError_t e = allow_smem<tree_kernel<D, BLK>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    // no more CTAs than runs of kMinTiles tiles (the most that the lengths allow)
+    // no more runs than tiles (the most that the lengths allow)
     const long long most = (long long)c.B * c.Hkv * ((c.T - c.n + kTile - 1) / kTile + 1);
-    const long long runs = (most + kMinTiles - 1) / kMinTiles;
     void *args[] = {&mq, &mk, &mv, &mk1, &mv1, &a};
     e = launch_early(reinterpret_cast<const void *>(tree_kernel<D, BLK>),
-                     dim3((unsigned)((runs < a.runs ? runs : a.runs) * a.nrt)), dim3(kThreads), C::SMEM, args, s);
+                     dim3((unsigned)((most < a.runs ? most : a.runs) * a.nrt)), dim3(kThreads), C::SMEM, args, s);
     if (e != cudaSuccess) return e;
     void *jargs[] = {&a};
     return launch_early(reinterpret_cast<const void *>(tree_join_kernel<D>),

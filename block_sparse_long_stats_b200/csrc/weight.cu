@@ -203,16 +203,6 @@ __device__ __forceinline__ void set_range(uint32_t (&m)[4], int lo, int hi) {
     }
 }
 
-// 16 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *x) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
-          "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
-        : "r"(taddr));
-}
-
 template <int D, int NC, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
