@@ -7,8 +7,9 @@
 // more, where an fp32 product is off by a hundredth of a radian, so the turn number
 // pos * freq / 2 pi is taken and reduced in fp64 and only the fraction goes to the fp32
 // sincospi. A thread therefore owns V pairs of one token (two 16-byte accesses a head)
-// and walks over the heads with one set of sines: the 8 fp64 reductions are spent
-// once per token and not once per head. Two heads' loads at a time in 64 registers (eight
+// and walks over up to 16 heads with one set of sines: the 8 fp64 reductions are spent
+// once per token and group of heads, three times for 32 + 8 heads and once per head only
+// where there are too few tokens to fill the GPU. Two heads' loads at a time in 64 registers (eight
 // CTAs per SM) rotate a 32K prompt of 32 + 8 heads in 127 us (5.3 TB/s, 80 % of the measured
 // copy bandwidth); four at a time in 128 registers took 178 us.
 #include <math.h>

@@ -8,10 +8,13 @@
 // with a few drafted tokens is bound by the bytes of K and V (512 per key at d = 128 against
 // 4 G n d flops); from about 200 rows on the tensor cores and the exponentials take as long.
 //
-// Work is counted in tiles of 128 keys (kept blocks of the list, closed up; the tree
-// itself is the last tile of its sequence). The tiles of all (b, kv-head) units in a row
-// are cut into equal runs, whatever the sequences' lengths: a run may end inside a unit
-// and go on in the next one. A run is a CTA per row tile; these stand next to each other in
+// Work is counted in tiles of 128 keys of text (the tree itself is the last tile of its
+// sequence). The tiles of all (b, kv-head) units in a row are cut into equal runs, whatever
+// the sequences' lengths: a run may end inside a unit and go on in the next one. Of its
+// stretch of text a run reads the kept blocks alone, closed up to tiles again, so its
+// work is what the lists keep there: with blocks kept at random 61 tiles at most where
+// the mean is 56 (16 nodes below), 14 where it is 10.5 (64 nodes), and further apart the
+// more the kept blocks cluster. A run is a CTA per row tile; these stand next to each other in
 // the grid and read the same K and V at the same time, so that they cross HBM once. A unit
 // that lies in several runs leaves one (m, l, O) state per run in the workspace, and a
 // second kernel joins them.
@@ -23,11 +26,18 @@
 //   warp 4    : TMA producer (Q per unit; K and V tiles)
 //   warp 5    : TMEM allocator and tcgen05.mma issuer
 //
-// Measured (B200, main kernel): 16 nodes, 32/8 heads over four 128K caches, half of the
-// 16-key blocks kept: 196-200 us, 5.4 TB/s of kept K and V (and slower under the power cap:
-// half of the products' rows are empty). 64 nodes over 32K: 47-49 us; 33 nodes, 40/8 heads
-// over eight ragged caches of up to 16000 keys: 102-108 us; there a tile takes 4600 cycles
-// with two CTAs on the SM: 2500 of softmax, 2000 for the products, which wait for one another.
+// P is rounded to bf16 for the second product, as in prefill: V is bf16, and both operands
+// of a product have one type. Against fp64 the output is then off by 2.1e-3 (7 nodes) to
+// 2.3e-3 of its norm, 1.66e-3 of which is its own rounding. P as the sum of two bf16 halves
+// (twice the products) left 1.66e-3 and took 280 us a call where this takes 227 (16 nodes,
+// long runs), and 66 against 57 (64 nodes).
+//
+// Measured (B200, main kernel, ten calls one after another; in brackets alone and cold):
+// 16 nodes, 32/8 heads over four 128K caches, half of the 16-key blocks kept: 200 us, 5.4
+// TB/s of kept K and V (up to 30 more in long runs under the power cap: half of the products'
+// rows are empty). 64 nodes over 32K: 49 us (52); 33 nodes, 40/8 heads over eight ragged
+// caches with 343 MB of K and V: 106 us (114); there a tile takes 4600 cycles with two CTAs
+// on the SM: 2500 of softmax, 2000 for the products, which wait for one another.
 // Tried: runs of two and four blocks copied in boxes of their own too (210 us for the first
 // case: the longer issuing loop costs more than the fewer boxes save), one CTA per SM with two
 // softmax warpgroups and deeper rings (107 us for the last case with one MMA warp, 117 with
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                       scale2, f32x2(nb, nb)), y0, y1);
                                 const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
                                 sp[e & 3] = add_f32x2(sp[e & 3], f32x2(p0, p1));
-                                w[e] = pack_bf16x2(p0, p1);     // P to bf16 for the tensor cores
+                                w[e] = pack_bf16x2(p0, p1);     // P to bf16 (see the head of the file)
                             }
                             tmem_st16(t_s + c * 16, w);
                         }

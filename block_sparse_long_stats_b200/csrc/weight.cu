@@ -26,9 +26,11 @@
 //
 // Measured (B200): a decode step's weight over four 128K caches with three quarters of the
 // blocks kept 142 us (5.9 TB/s, 90 % of the measured copy bandwidth; weight_few_kernel),
-// 128 queries over 32K keys 53 us, all queries of a 4K prompt 98 us; in the last two ex2
-// is busy 57 % of the time and a scheduler issues 38 %: what is left is the latency of the
-// sums. Tried: a product of N = 128 for each warpgroup of a score tile, begun as soon as its own
+// 128 queries over 32K keys 54 us, all queries of a 4K prompt 99 us (53 and 98 before the
+// columns of queries that saw nothing were masked; carrying whether there are any on the
+// barrier of the columns' lse took as long). In the last two ex2 is busy 54-57 % of
+// the time and a scheduler issues 37 %: what is left is the latency of the
+// sums. Tried, against 53 and 98: a product of N = 128 for each warpgroup of a score tile, begun as soon as its own
 // half is read (59 us for the window: the products take longer than what the early start
 // gains), the columns' lse in two buffers with one barrier instead of two (53.4 and 99), all four
 // warpgroups on one score tile, 64 columns each, the other tile multiplied meanwhile (61 and

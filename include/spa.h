@@ -481,12 +481,15 @@ spa_status spa_prefill_host(const void *q, const void *k, const void *v, void *o
  * spa_rope_frequencies fills freqs[rot/2] (radians per position, host memory) and
  * *mscale for
  *   SPA_ROPE_NONE    freqs[c] = base^(-2c/rot), mscale = 1
- *   SPA_ROPE_LINEAR  those over `factor` (positions interpolated)
+ *   SPA_ROPE_LINEAR  those over `factor` (positions interpolated, as in "Extending Context
+ *                    Window of Large Language Models via Positional Interpolation")
  *   SPA_ROPE_NTK     base replaced by base * factor^(rot/(rot-2)): the slowest pair is
  *                    interpolated, the fastest kept
  *   SPA_ROPE_PARTS   pairs that turn at least `fast` times over the trained length are
  *                    kept, those that turn at most `slow` times interpolated, a linear
- *                    ramp over c between; mscale = 1 + 0.1 ln(factor)
+ *                    ramp over c between; mscale = 1 + 0.1 ln(factor). The frequencies
+ *                    "by parts" and the factor of "YaRN: Efficient Context Window
+ *                    Extension of Large Language Models"; a ramp of no width gets 0.001
  *   rot: even, 2 .. 256 (NTK: at least 4); base > 1; factor >= 1; PARTS: trained > 0,
  *   fast > slow > 0 (ignored otherwise). SPA_ERR_INVALID if not. Touches no device.
  */
