@@ -258,3 +258,35 @@ def test_new_outputs_of_the_gather_are_zero_behind_the_list():
         at = keep.long()
         assert torch.equal(v[:, :, :7], vc.gather(2, at[..., None].expand(2, 2, 7, 128)))
         assert torch.equal(s[:, :, :7], score.gather(2, at))
+
+
+# ---------------------------------------------------------------- captured, on another stream
+
+@pytest.mark.parametrize("d,n,T,block", [(64, 20, 500, 32), (128, 9, 1200, 64), (128, 60, 70, 16)])
+def test_decode_tree_on_another_stream_and_replayed_from_a_graph(d, n, T, block):
+    # the last one: less text than a block
+    g = gen(81 + T)
+    q, kc, vc = randn(g, 2, 8, n, d), randn(g, 2, 2, T, d), randn(g, 2, 2, T, d)
+    parents = tree_of(g, 2, n)
+
+    def same(r):
+        at = torch.arange(want["idx"].shape[3], device="cuda") < want["count"][..., None]
+        assert torch.equal(r["idx"][at], want["idx"][at])
+        assert all(torch.equal(r[k], want[k]) for k in ("out", "lse", "count", "mean", "var"))
+
+    want = {k: v.clone() for k, v in spa.decode_tree(q, kc, vc, parents, block, 0.6, want_lse=True).items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = spa.decode_tree(q, kc, vc, parents, block, 0.6, want_lse=True, stream=side)
+    torch.cuda.synchronize()
+    same(r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = spa.decode_tree(q, kc, vc, parents, block, 0.6, want_lse=True)
+    for _ in range(2):
+        r["out"].zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    same(r)
+    ok()
